@@ -323,6 +323,129 @@ tsa_status tsa_index_overlap(const int32_t* idx, int32_t n_layers, int32_t units
 tsa_status tsa_reuse_policy(const double* M, int32_t n_layers, double theta, const uint8_t* force_full,
                             int32_t* source, int32_t* n_full, double* total_sim);
 
+/* ------------------------------------------------------------------ paged cache */
+
+/* The decode path over a cache in pages: queries and keys made (norm and position
+ * rotation), new keys and values appended, and attention that reads the pages
+ * where they lie, for each sequence alone or with a prefix that a batch shares read
+ * once for all.  These entry points take bf16 or fp16 (`dtype`, one type for
+ * Q, K, V and O), any GQA group of at most 16 heads, and write O in that type (it
+ * feeds the output projection); every sum is in fp32.  The conventions at the top
+ * hold otherwise: caller-owned device memory (of the current device), work
+ * enqueued on `stream`, argument errors before anything is enqueued, range errors
+ * that only the device sees skip the offending work and set the workspace's flag. */
+typedef enum { TSA_BF16 = 0, TSA_FP16 = 1 } tsa_dtype;
+
+/* Row j of (sequence b, kv-head h) is d elements at
+ *   page * page_stride + h * head_stride + (j % page_size) * row_stride
+ * of K and of V, with page = page_table[b * max_pages + j / page_size].  Strides are
+ * in elements and multiples of 8, and no two rows may overlap; K and V must be
+ * 16-byte aligned.  Heads before rows ([num_pages, Hkv, page_size, d]) and rows
+ * before heads ([num_pages, page_size, Hkv, d]) are both such caches, as are the two
+ * halves of one [num_pages, 2, Hkv, page_size, d] buffer.  A contiguous cache
+ * [B, Hkv, Ncap, d] with Ncap a multiple of 16 is the case num_pages = B,
+ * page_size = Ncap, page_table[b] = b: tsa_paged_append then feeds
+ * tsa_decode_step.  Table entries past a sequence's rows are not read. */
+typedef struct {
+    void* K;
+    void* V;
+    const int32_t* page_table; /* [B, max_pages] */
+    int64_t page_stride, head_stride, row_stride;
+    int32_t num_pages;         /* pages of K and V, >= 1 */
+    int32_t page_size;         /* rows of a page, a multiple of 16 */
+    int32_t max_pages;         /* width of the table */
+    int32_t B, Hkv;
+    int32_t d;                 /* 128 */
+    int32_t dtype;             /* tsa_dtype */
+} tsa_paged_cache;
+
+/* Position rotation of the first rot_dim elements of a head (the rest stay):
+ * pair i, (x[i], x[i + rot_dim/2]) or, interleaved, (x[2i], x[2i + 1]), turns by
+ * position * inv_freq[i] radians.  rot_dim is a multiple of 16 from 0 (no rotation) to 128.
+ * inv_freq is [rot_dim / 2] float64 on the device (any base or scaling of
+ * the frequencies is the caller's table); the angle is formed in 64 bits. */
+typedef struct {
+    const double* inv_freq;
+    int32_t rot_dim;
+    int32_t interleaved;
+} tsa_rotation;
+
+/* Queries and keys of T tokens in one pass: the RMS norm of each head (over its d
+ * elements, times a weight [d] fp32; a NULL weight leaves those heads unnormed), then
+ * the rotation.  One rounding, at the end.  Heads of 128 elements at
+ * token * stride_t + head * stride_h (elements, multiples of 8; 16-byte aligned
+ * bases), so the queries and keys of one fused projection are read in place; an
+ * output may be its own input (the same pointer and strides), and must not
+ * overlap the inputs otherwise.  Hq or Hkv may be 0. */
+typedef struct {
+    const void *q, *k;                    /* [T, Hq, d], [T, Hkv, d] */
+    void *q_out, *k_out;
+    int64_t q_stride_t, q_stride_h, k_stride_t, k_stride_h;
+    int64_t q_out_stride_t, q_out_stride_h, k_out_stride_t, k_out_stride_h;
+    const float *q_weight, *k_weight;     /* [d] or NULL, 16-byte aligned */
+    const int32_t* positions;             /* [T]; NULL only with rot_dim = 0 */
+    tsa_rotation rot;
+    int32_t T, Hq, Hkv, d, dtype;
+    float eps;                            /* >= 0 */
+} tsa_qk_args;
+tsa_status tsa_qk_norm_rope(const tsa_qk_args* args, void* stream);
+
+/* Append T tokens' keys and values to a paged cache, one token or whole prompts:
+ * token t goes to row row[t] of sequence seq[t] (seq NULL: sequence t, T <= B).  Its
+ * key heads are rotated on the way by positions[t] (NULL: row[t]), its value
+ * heads copied.  seq[t] < 0 is padding: the token is skipped.  A sequence, row or page
+ * out of range is skipped and sets the device flag.  The tokens' (sequence, row)
+ * pairs, and the pages behind them, must be distinct: of two tokens sent to one
+ * row, which one's elements land is not defined.  K and V must not overlap the
+ * cache.  ws: at least 256 bytes. */
+typedef struct {
+    tsa_paged_cache cache;
+    const void *K, *V;                    /* [T, Hkv, d] */
+    int64_t k_stride_t, k_stride_h, v_stride_t, v_stride_h;
+    const int32_t *seq, *row, *positions; /* [T]; seq, positions may be NULL */
+    tsa_rotation rot;
+    int32_t T;
+    void* ws;
+    size_t ws_bytes;
+} tsa_append_args;
+tsa_status tsa_paged_append(const tsa_append_args* args, void* stream);
+
+/* Bytes of workspace that tsa_paged_attn (prefix_len = 0) or tsa_prefix_attn needs for
+ * this cache and Hq query heads; Hq = 0: what tsa_paged_append needs.  A larger
+ * prefix_len never needs less.  Returns 0 on invalid arguments.  Zero it once with
+ * tsa_workspace_init; the calls leave it ready for the next.  The two calls may
+ * share one; calls that share one must be ordered on one stream.  (It is not laid
+ * out as tsa_workspace_size's: do not share it with tsa_decode_step.) */
+size_t tsa_paged_workspace_size(const tsa_paged_cache* cache, int32_t Hq, int32_t prefix_len);
+
+typedef struct {
+    tsa_paged_cache cache;
+    const void* Q;              /* [B, Hq, d], contiguous */
+    const int32_t* seq_lens;    /* [B], 0 <= len_b <= max_pages * page_size */
+    const int32_t* idx;         /* NULL: every row; else [B, Hkv, k_max] rows, entries < 0 skipped */
+    const int32_t* k_per_seq;   /* [B] or NULL (= k_max): entries of idx used, min(k, len_b) of them */
+    void* O;                    /* [B, Hq, d] in dtype; 0 for a sequence without a row */
+    float* lse;                 /* NULL or [B, Hq]: base-2 log-sum-exp of the scaled logits (-inf without a row) */
+    int32_t Hq, k_max;
+    int32_t prefix_len;         /* tsa_prefix_attn: the rows that the batch shares */
+    float scale;                /* finite, > 0 */
+    void* ws;
+    size_t ws_bytes;
+} tsa_paged_attn_args;
+
+/* One token per sequence over its pages: every row, or (a layer that reuses
+ * an earlier layer's indices) the rows of an index list as tsa_decode_step writes it.
+ * prefix_len must be 0. */
+tsa_status tsa_paged_attn(const tsa_paged_attn_args* args, void* stream);
+
+/* The same over every row (idx NULL) for a batch whose sequences begin with the
+ * same prefix_len rows: the prefix's K and V are read once for all sequences that
+ * hold it whole (len_b >= prefix_len), through the table of the first of them; what
+ * follows is read through each sequence's own table.  A sequence shorter than the
+ * prefix (or a padding slot with len_b = 0) is attended through its own table alone.
+ * The result is tsa_paged_attn's, up to rounding.  prefix_len = 0: no shared rows. */
+tsa_status tsa_prefix_attn(const tsa_paged_attn_args* args, void* stream);
+
 /* ------------------------------------------------------------------ status */
 
 /* Wait for `stream`, then read and clear the device error flag in `ws`:

@@ -269,3 +269,68 @@ def decode_step(Q, K, V, seq_lens, kreq, k_max: int, scale: float, mode: int = 1
     idx = topk(S, nrows, kreq, k_max, units)
     O = attn(Q, K, V, seq_lens, idx, kreq, k_max, block, scale, units)
     return O, idx, S
+
+
+# ------------------------------------------------------------------ the paged decode path (numpy, float64)
+
+def _f64(t) -> np.ndarray:
+    return t.detach().cpu().to(torch.float64).numpy()
+
+
+def rotate(x: np.ndarray, positions, inv_freq, interleaved: bool) -> np.ndarray:
+    """Position rotation of x [T, H, d]: the pairs of its first 2 * len(inv_freq) elements, as
+    complex numbers, times exp(i * position * inv_freq)."""
+    f = np.asarray(inv_freq, dtype=np.float64)
+    n = f.size
+    turn = np.exp(1j * np.asarray(positions, dtype=np.float64)[:, None] * f)[:, None, :]
+    y = np.array(x, dtype=np.float64)
+    a, b = (slice(0, 2 * n, 2), slice(1, 2 * n, 2)) if interleaved else (slice(0, n), slice(n, 2 * n))
+    z = (x[..., a] + 1j * x[..., b]) * turn
+    y[..., a], y[..., b] = z.real, z.imag
+    return y
+
+
+def norm_rope(x: torch.Tensor, weight, eps: float, positions, inv_freq, interleaved: bool) -> np.ndarray:
+    """RMS norm of each head of x [T, H, d] (weight None: none), then the rotation (inv_freq None: none)."""
+    y = _f64(x)
+    if weight is not None:
+        y = y / np.sqrt((y * y).mean(-1, keepdims=True) + eps) * _f64(weight)
+    return y if inv_freq is None else rotate(y, positions, _f64(inv_freq), interleaved)
+
+
+def paged_rows(pages: torch.Tensor, table, b: int, rows) -> np.ndarray:
+    """Rows of sequence b out of pages [num_pages, Hkv, page_size, d]: [Hkv, len(rows), d] float64."""
+    size = pages.shape[2]
+    out = [_f64(pages[int(table[b][r // size]), :, r % size]) for r in map(int, rows)]
+    return np.stack(out, 1) if out else np.zeros((pages.shape[1], 0, pages.shape[3]))
+
+
+def paged_attn(Q, K_pages, V_pages, table, seq_lens, scale: float, idx=None, k_per_seq=None):
+    """One token per sequence over its pages: (O [B, Hq, d], lse [B, Hq] in base 2), both float64.
+    idx [B, Hkv, k]: the rows attended (negative entries skipped), the first
+    min(k_per_seq[b], len_b) of them."""
+    q = _f64(Q)
+    B, Hq, d = q.shape
+    Hkv = K_pages.shape[1]
+    g = Hq // Hkv
+    O, lse = np.zeros((B, Hq, d)), np.full((B, Hq), -np.inf)
+    for b in range(B):
+        n = int(seq_lens[b])
+        if idx is None:
+            K, V = paged_rows(K_pages, table, b, range(n)), paged_rows(V_pages, table, b, range(n))
+        for h in range(Hkv):
+            if idx is None:
+                k, v = K[h], V[h]
+            else:
+                kb = min(n, idx.shape[2] if k_per_seq is None else int(k_per_seq[b]))
+                rows = [int(r) for r in idx[b, h, :kb] if r >= 0]
+                k, v = paged_rows(K_pages, table, b, rows)[h], paged_rows(V_pages, table, b, rows)[h]
+            if k.shape[0] == 0:
+                continue
+            s = (q[b, h * g:(h + 1) * g] @ k.T) * scale
+            m = s.max(-1, keepdims=True)
+            p = np.exp(s - m)
+            l = p.sum(-1, keepdims=True)
+            O[b, h * g:(h + 1) * g] = p @ v / l
+            lse[b, h * g:(h + 1) * g] = ((m + np.log(l)) / np.log(2.0))[:, 0]
+    return O, lse

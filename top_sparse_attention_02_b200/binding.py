@@ -45,6 +45,7 @@ EARLY_INPUTS = 2  # tsa_step_args.flags: the kernel before the step writes none 
 
 
 _vp, _sz, _i32, _f32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.c_float
+_i64 = ctypes.c_int64
 _SIGS = {
     "tsa_workspace_size": (_sz, [tsa_shape, _i32, _i32, _i32]),
     "tsa_workspace_init": (ctypes.c_int, [_vp, _sz, _vp]),
@@ -268,3 +269,228 @@ def hbm_gather(base, rows, ws, stream=None):
     """Gather the 256-byte rows `rows` (int32, device) of `base` (the probe; nothing is kept)."""
     nbytes = base.numel() * base.element_size()
     _ok(_lib.tsa_hbm_gather(_ptr(base), nbytes, _ptr(rows), rows.numel(), *_wsargs(ws), _stream(stream)))
+
+
+# ------------------------------------------------------------------ paged cache
+
+class tsa_paged_cache(ctypes.Structure):
+    _fields_ = [("K", _vp), ("V", _vp), ("page_table", _vp), ("page_stride", _i64), ("head_stride", _i64),
+                ("row_stride", _i64), ("num_pages", _i32), ("page_size", _i32), ("max_pages", _i32), ("B", _i32),
+                ("Hkv", _i32), ("d", _i32), ("dtype", _i32)]
+
+
+class tsa_rotation(ctypes.Structure):
+    _fields_ = [("inv_freq", _vp), ("rot_dim", _i32), ("interleaved", _i32)]
+
+
+class tsa_qk_args(ctypes.Structure):
+    _fields_ = [("q", _vp), ("k", _vp), ("q_out", _vp), ("k_out", _vp), ("q_stride_t", _i64), ("q_stride_h", _i64),
+                ("k_stride_t", _i64), ("k_stride_h", _i64), ("q_out_stride_t", _i64), ("q_out_stride_h", _i64),
+                ("k_out_stride_t", _i64), ("k_out_stride_h", _i64), ("q_weight", _vp), ("k_weight", _vp),
+                ("positions", _vp), ("rot", tsa_rotation), ("T", _i32), ("Hq", _i32), ("Hkv", _i32), ("d", _i32),
+                ("dtype", _i32), ("eps", _f32)]
+
+
+class tsa_append_args(ctypes.Structure):
+    _fields_ = [("cache", tsa_paged_cache), ("K", _vp), ("V", _vp), ("k_stride_t", _i64), ("k_stride_h", _i64),
+                ("v_stride_t", _i64), ("v_stride_h", _i64), ("seq", _vp), ("row", _vp), ("positions", _vp),
+                ("rot", tsa_rotation), ("T", _i32), ("ws", _vp), ("ws_bytes", _sz)]
+
+
+class tsa_paged_attn_args(ctypes.Structure):
+    _fields_ = [("cache", tsa_paged_cache), ("Q", _vp), ("seq_lens", _vp), ("idx", _vp), ("k_per_seq", _vp),
+                ("O", _vp), ("lse", _vp), ("Hq", _i32), ("k_max", _i32), ("prefix_len", _i32), ("scale", _f32),
+                ("ws", _vp), ("ws_bytes", _sz)]
+
+
+for _name, _argtypes, _res in (("tsa_qk_norm_rope", [ctypes.POINTER(tsa_qk_args), _vp], ctypes.c_int),
+                               ("tsa_paged_append", [ctypes.POINTER(tsa_append_args), _vp], ctypes.c_int),
+                               ("tsa_paged_workspace_size", [ctypes.POINTER(tsa_paged_cache), _i32, _i32], _sz),
+                               ("tsa_paged_attn", [ctypes.POINTER(tsa_paged_attn_args), _vp], ctypes.c_int),
+                               ("tsa_prefix_attn", [ctypes.POINTER(tsa_paged_attn_args), _vp], ctypes.c_int)):
+    _f = getattr(_lib, _name)
+    _f.restype, _f.argtypes = _res, _argtypes
+
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+
+
+def _need(ok: bool, msg: str):
+    if not ok:
+        raise TsaError(TSA_ERR_INVALID_ARG, msg)
+
+
+def _tensor(t, what: str, dtype, shape, device, contiguous: bool = True):
+    """t is a tensor of this type, shape (None: any size) and device; contiguous, or
+    with contiguous elements in its last dimension."""
+    _need(isinstance(t, torch.Tensor) and t.dtype == dtype, f"{what} must be a {dtype} tensor")
+    _need(t.dim() == len(shape) and all(n is None or n == m for n, m in zip(shape, t.shape)),
+          f"{what} must have the shape {list(shape)} (got {list(t.shape)})")
+    _need(t.device == device, f"{what} is on {t.device}, not {device}")
+    if contiguous:
+        _need(t.is_contiguous(), f"{what} must be contiguous")
+    else:
+        _need(t.shape[-1] == 1 or t.stride(-1) == 1, f"{what}: the last dimension must be contiguous")
+
+
+def _hold(a, device, *tensors):
+    """The arguments keep their tensors alive and remember their device."""
+    a._tensors, a._device = tensors, device
+    return a
+
+
+def _launch(fn, a, stream):
+    """Enqueue on `stream` (None: torch's current stream on the tensors' device), with
+    that device current."""
+    dev = a._device
+    if dev.type != "cuda" or dev.index == torch.cuda.current_device():
+        _ok(fn(ctypes.byref(a), _stream(stream)))
+        return
+    with torch.cuda.device(dev):
+        _ok(fn(ctypes.byref(a), _stream(stream)))
+
+
+def paged_cache(K_pages, V_pages, page_table) -> tsa_paged_cache:
+    """A cache in pages: K_pages, V_pages [num_pages, Hkv, page_size, 128] bf16 or fp16 with
+    the same strides (a pool laid out row by row is passed as pool.permute(0, 2, 1, 3)),
+    page_table [B, max_pages] int32."""
+    _need(isinstance(K_pages, torch.Tensor) and K_pages.dtype in _DTYPES, "K_pages must be a bf16 or fp16 tensor")
+    dev = K_pages.device
+    _tensor(K_pages, "K_pages", K_pages.dtype, (None,) * 4, dev, contiguous=False)
+    _tensor(V_pages, "V_pages", K_pages.dtype, K_pages.shape, dev, contiguous=False)
+    _need(K_pages.stride() == V_pages.stride(), "K_pages and V_pages must have the same strides")
+    _tensor(page_table, "page_table", torch.int32, (None, None), dev)
+    c = tsa_paged_cache()
+    c.K, c.V, c.page_table = K_pages.data_ptr(), V_pages.data_ptr(), page_table.data_ptr()
+    c.page_stride, c.head_stride, c.row_stride = K_pages.stride()[:3]
+    c.num_pages, c.Hkv, c.page_size, c.d = K_pages.shape
+    c.B, c.max_pages = page_table.shape
+    c.dtype = _DTYPES[K_pages.dtype]
+    c._torch_dtype = K_pages.dtype
+    return _hold(c, dev, K_pages, V_pages, page_table)
+
+
+def paged_workspace_size(cache: tsa_paged_cache, Hq: int = 0, prefix_len: int = 0) -> int:
+    n = _lib.tsa_paged_workspace_size(ctypes.byref(cache), Hq, prefix_len)
+    if n == 0:
+        raise TsaError(TSA_ERR_INVALID_ARG, last_error())
+    return int(n)
+
+
+def new_paged_workspace(cache: tsa_paged_cache, Hq: int = 0, prefix_len: int = 0) -> torch.Tensor:
+    """Allocate (with torch) and zero a workspace for paged_attn / prefix_attn with Hq query
+    heads (Hq = 0: for paged_append), on the cache's device."""
+    ws = torch.empty(paged_workspace_size(cache, Hq, prefix_len), dtype=torch.uint8, device=cache._device)
+    with torch.cuda.device(cache._device):
+        workspace_init(ws)
+    return ws
+
+
+def _rotation(inv_freq, interleaved: bool, device) -> tsa_rotation:
+    r = tsa_rotation()
+    if inv_freq is not None:
+        _tensor(inv_freq, "inv_freq", torch.float64, (None,), device)
+        r.inv_freq, r.rot_dim = inv_freq.data_ptr(), 2 * inv_freq.numel()
+    r.interleaved = int(interleaved)
+    return r
+
+
+def qk_norm_rope_args(q, k, q_out, k_out, *, q_weight=None, k_weight=None, eps: float = 1e-6, positions=None,
+                      inv_freq=None, interleaved: bool = False) -> tsa_qk_args:
+    """Arguments of qk_norm_rope: q [T, Hq, 128], k [T, Hkv, 128] (either may be None) of any
+    token and head strides, their outputs (which may be q and k), norm weights [128] fp32
+    (None: no norm), positions [T] int32 and inv_freq [rot_dim / 2] float64 (None: no rotation)."""
+    some = q if q is not None else k
+    _need(isinstance(some, torch.Tensor) and some.dtype in _DTYPES and some.dim() == 3,
+          "q or k must be a bf16 or fp16 tensor [T, heads, 128]")
+    dev, T, d = some.device, some.shape[0], some.shape[2]
+    a = tsa_qk_args()
+    for x, out, w, n in ((q, q_out, q_weight, "q"), (k, k_out, k_weight, "k")):
+        if x is None:
+            _need(out is None and w is None, f"{n} is None, but {n}_out or {n}_weight is not")
+            continue
+        _tensor(x, n, some.dtype, (T, None, d), dev, contiguous=False)
+        _tensor(out, n + "_out", some.dtype, x.shape, dev, contiguous=False)
+        if w is not None:
+            _tensor(w, n + "_weight", torch.float32, (d,), dev)
+        setattr(a, n, x.data_ptr())
+        setattr(a, n + "_out", out.data_ptr())
+        setattr(a, n + "_weight", _ptr(w))
+        for name, t in ((n, x), (n + "_out", out)):
+            setattr(a, name + "_stride_t", t.stride(0))
+            setattr(a, name + "_stride_h", t.stride(1))
+    a.rot = _rotation(inv_freq, interleaved, dev)
+    if positions is not None:
+        _tensor(positions, "positions", torch.int32, (T,), dev)
+        a.positions = positions.data_ptr()
+    a.T, a.d, a.dtype, a.eps = T, d, _DTYPES[some.dtype], eps
+    a.Hq, a.Hkv = 0 if q is None else q.shape[1], 0 if k is None else k.shape[1]
+    return _hold(a, dev, q, k, q_out, k_out, q_weight, k_weight, positions, inv_freq)
+
+
+def qk_norm_rope(args: tsa_qk_args, stream=None):
+    """The norms of each query and key head, and their rotation, in one pass."""
+    _launch(_lib.tsa_qk_norm_rope, args, stream)
+
+
+def paged_append_args(cache: tsa_paged_cache, K, V, row, ws, *, seq=None, positions=None, inv_freq=None,
+                      interleaved: bool = False) -> tsa_append_args:
+    """Arguments of paged_append: K, V [T, Hkv, 128] of any token and head strides; row,
+    seq (None: token t is sequence t's) and positions (None: row) are [T] int32."""
+    dev = cache._device
+    a = tsa_append_args()
+    a.cache = cache
+    _tensor(K, "K", cache._torch_dtype, (None, cache.Hkv, cache.d), dev, contiguous=False)
+    _tensor(V, "V", cache._torch_dtype, K.shape, dev, contiguous=False)
+    T = K.shape[0]
+    for n, t in (("row", row), ("seq", seq), ("positions", positions)):
+        if t is not None or n == "row":
+            _tensor(t, n, torch.int32, (T,), dev)
+            setattr(a, n, t.data_ptr())
+    _tensor(ws, "ws", torch.uint8, (None,), dev)
+    a.K, a.V, a.T = K.data_ptr(), V.data_ptr(), T
+    a.k_stride_t, a.k_stride_h, a.v_stride_t, a.v_stride_h = K.stride(0), K.stride(1), V.stride(0), V.stride(1)
+    a.rot = _rotation(inv_freq, interleaved, dev)
+    a.ws, a.ws_bytes = _wsargs(ws)
+    return _hold(a, dev, cache, K, V, row, ws, seq, positions, inv_freq)
+
+
+def paged_append(args: tsa_append_args, stream=None):
+    """New keys, rotated on the way, and values into the cache's pages."""
+    _launch(_lib.tsa_paged_append, args, stream)
+
+
+def paged_attn_args(cache: tsa_paged_cache, Q, seq_lens, O, ws, *, scale: float, idx=None, k_per_seq=None,
+                    prefix_len: int = 0, lse=None) -> tsa_paged_attn_args:
+    """Arguments of paged_attn and prefix_attn: Q, O [B, Hq, 128] in the cache's type, seq_lens
+    [B] int32; idx [B, Hkv, k_max] int32 with k_per_seq [B] (paged_attn), or prefix_len
+    (prefix_attn); lse [B, Hq] fp32 or None."""
+    dev = cache._device
+    a = tsa_paged_attn_args()
+    a.cache = cache
+    _tensor(Q, "Q", cache._torch_dtype, (cache.B, None, cache.d), dev)
+    _tensor(O, "O", cache._torch_dtype, Q.shape, dev)
+    _tensor(seq_lens, "seq_lens", torch.int32, (cache.B,), dev)
+    if idx is not None:
+        _tensor(idx, "idx", torch.int32, (cache.B, cache.Hkv, None), dev)
+        a.idx, a.k_max = idx.data_ptr(), idx.shape[2]
+    if k_per_seq is not None:
+        _tensor(k_per_seq, "k_per_seq", torch.int32, (cache.B,), dev)
+        a.k_per_seq = k_per_seq.data_ptr()
+    if lse is not None:
+        _tensor(lse, "lse", torch.float32, Q.shape[:2], dev)
+        a.lse = lse.data_ptr()
+    _tensor(ws, "ws", torch.uint8, (None,), dev)
+    a.Q, a.O, a.seq_lens = Q.data_ptr(), O.data_ptr(), seq_lens.data_ptr()
+    a.Hq, a.prefix_len, a.scale = Q.shape[1], prefix_len, scale
+    a.ws, a.ws_bytes = _wsargs(ws)
+    return _hold(a, dev, cache, Q, seq_lens, O, ws, idx, k_per_seq, lse)
+
+
+def paged_attn(args: tsa_paged_attn_args, stream=None):
+    """One token per sequence over its pages: every row, or the rows of idx."""
+    _launch(_lib.tsa_paged_attn, args, stream)
+
+
+def prefix_attn(args: tsa_paged_attn_args, stream=None):
+    """One token per sequence, the rows [0, prefix_len) that the batch shares read once for all."""
+    _launch(_lib.tsa_prefix_attn, args, stream)

@@ -1,0 +1,674 @@
+// paged.cu -- decode attention of one token per sequence over a paged cache:
+// every row of each sequence, or the rows an index list names; optionally on top
+// of partials that another pass made over a prefix all sequences share.
+//
+//   O = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * <q_h, k_j> - m)
+// as flash decoding: running maximum m and sum per head in fp32, one pass over
+// the rows, the parts of a unit (sequence, kv-head) joined by
+//   O = sum_i 2^(M_i - M) acc_i / sum_i 2^(M_i - M) L_i.
+//
+// A row is read once for g <= 16 query heads (at most 16 flop a byte), so HBM
+// bounds it, and two things decide how near it comes: every SM streaming until
+// the end, and enough bytes in flight.
+//  - Even work whatever the lengths: the granules (64 rows) of all units are
+//    laid end to end and each CTA takes the same number of them, so a CTA may end
+//    in the middle of one unit and begin in the middle of another.  The lengths
+//    are on the device only; each CTA adds them up itself.  A unit that lies in
+//    one CTA is finished there; otherwise each CTA writes its piece and the last
+//    to arrive (a counter per unit, which it sets back to zero) joins them in the
+//    order of the CTAs, so that the result does not depend on who was last.
+//  - Each of a CTA's 4 warps streams its own 16 rows of every granule through
+//    its own ring of 8 KB stages (K and V of 16 rows), so a warp never waits for
+//    another one until the unit ends.  Two CTAs an SM.  Every row: two 2-D boxes
+//    each of K and V (64 elements x 16 rows, 128-byte swizzle) by TMA; a page
+//    holds a multiple of 16 rows, so a tile never crosses pages and any order of
+//    heads and rows inside the page is a matter of the tensor map's strides.
+//    Selected rows: cp.async, 16 bytes a lane, into the same swizzled layout.
+//  - The products run on mma.sync with the 16 rows as M and the group's heads as
+//    N (8, or 16 for groups above 8): S^T = K Q^T, O^T += V^T P^T.  P is kept as
+//    two numbers of the element type (its rounding and the rest), so the weights
+//    keep about 16 bits and the output's own rounding is the larger error; the
+//    second product costs little in a kernel that waits for memory.
+//
+// Rows outside the sequence in a tile that is partly valid: their scores become
+// -inf, and their V rows are overwritten with zeros in shared memory (0 * NaN in
+// memory nobody wrote would be NaN).
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "common.cuh"
+#include "paged.cuh"
+#include "tma.cuh"
+
+namespace tsa {
+
+constexpr int kPgWarps = 4;
+constexpr int kPgThreads = kPgWarps * 32;
+constexpr int kPgGranule = kPgWarps * kPageRows;   // rows
+constexpr int kPgHalf = kPageRows * 128;           // 64 elements of 16 rows: 2 KB
+constexpr int kPgStage = 4 * kPgHalf;              // K halves, V halves: 8 KB
+constexpr int kPgCtasPerSm = 2;
+constexpr float kNegInf = -INFINITY;
+
+template <int NT>
+struct PgCfg {
+    static constexpr int kStages = NT == 1 ? 3 : 2;
+    static constexpr int kHeads = NT * 8;
+    // all of it dynamic (1024-byte aligned): rings, merge buffer, barriers and scalars.
+    // Two CTAs of 115,360 B (one n-tile) and their 1 KB each fit an SM's 228 KB.
+    static constexpr int kMerge = kPgWarps * kStages * kPgStage;
+    static constexpr int kBars = kMerge + kPgWarps * kHeads * kPartFloats * 4;
+    static constexpr int kScan = kBars + kPgWarps * kStages * 8;
+    static constexpr int kSmem = kScan + kPgWarps * 8 + 32;
+};
+
+int paged_ctas() { return kPgCtasPerSm * kPagedSms; }
+
+// Where a sequence's rows begin and end for this pass, in granules of 64 rows.
+struct Span {
+    int lo, hi;  // rows [lo, hi) (selected rows: entries of the list)
+    __device__ __forceinline__ int first() const { return lo / kPgGranule; }
+    __device__ __forceinline__ int granules() const { return hi > lo ? (hi + kPgGranule - 1) / kPgGranule - first() : 0; }
+};
+
+struct PgArgs {
+    Pages c;
+    const uint16_t* Q;
+    int Hq, G;
+    const int32_t *lens, *idx, *kreq;
+    int k_max;
+    float scale_log2;  // scale * log2(e)
+    uint16_t* O;
+    float* lse;
+    float* pieces;       // [2 * gridDim.x][G][kPartFloats]
+    unsigned* counters;  // [B * Hkv], zero between calls
+    PrefixParts pre;
+    unsigned* flag;
+};
+
+template <bool GATHER>
+__device__ __forceinline__ Span span_of(const PgArgs& a, int b, bool report) {
+    int len = a.lens[b];
+    const int cap = a.c.rows_cap();
+    if (len < 0 || len > cap) {
+        if (report) atomicOr(a.flag, kFlagBounds);
+        len = len < 0 ? 0 : cap;
+    }
+    Span s;
+    s.lo = 0;
+    s.hi = len;
+    if constexpr (GATHER) {
+        int k = a.kreq ? a.kreq[b] : a.k_max;
+        if (k < 0 || k > a.k_max) {
+            if (report && (k < 0 || min(k, len) > a.k_max)) atomicOr(a.flag, kFlagBounds);
+            k = k < 0 ? 0 : a.k_max;
+        }
+        s.hi = min(k, len);
+    } else if (a.pre.splits > 0 && len >= a.pre.prefix_len) {
+        s.lo = a.pre.prefix_len;
+    }
+    return s;
+}
+
+// Join parts of one (b, kv-head): n0 of them `part0` apart from `p0` (the prefix's
+// splits), n1 of them listed by slot(i) (the CTAs' pieces), each [G][kPartFloats]
+// with M and L after the 128 sums; write O and lse.  All threads of the CTA.
+template <class E, class Slot>
+__device__ void finish(const PgArgs& a, int b, int h, int n0, const float* p0, long long part0, int n1, Slot slot,
+                       float* wts) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = n0 + n1;
+    auto part = [&](int i) { return i < n0 ? p0 + i * part0 : slot(i - n0); };
+    for (int g = warp; g < a.G; g += kPgWarps) {
+        float M = kNegInf;
+        for (int i = lane; i < n; i += 32) {
+            const float* p = part(i) + g * kPartFloats;
+            if (__ldcg(p + kD + 1) > 0.f) M = fmaxf(M, __ldcg(p + kD));
+        }
+#pragma unroll
+        for (int m = 16; m; m >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
+        float L = 0.f;
+        bool bad = false;  // a NaN sum: the result is NaN, as the softmax's is
+        for (int i = lane; i < n; i += 32) {
+            const float* p = part(i) + g * kPartFloats;
+            const float l = __ldcg(p + kD + 1), w = l > 0.f ? exp2f(__ldcg(p + kD) - M) : 0.f;
+            bad |= l != l;
+            wts[g * n + i] = w;
+            L += w * l;
+        }
+#pragma unroll
+        for (int m = 16; m; m >>= 1) L += __shfl_xor_sync(0xffffffffu, L, m);
+        if (__any_sync(0xffffffffu, bad)) L = NAN;
+        __syncwarp();
+        const float inv = L == 0.f ? 0.f : 1.0f / L;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const float w = wts[g * n + i];
+            if (w == 0.f) continue;  // (a part without a row holds no sums)
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(part(i) + g * kPartFloats) + lane);
+            acc.x = fmaf(w, v.x, acc.x), acc.y = fmaf(w, v.y, acc.y);
+            acc.z = fmaf(w, v.z, acc.z), acc.w = fmaf(w, v.w, acc.w);
+        }
+        const long long row = (long long)b * a.Hq + h * a.G + g;
+        uint2 o;
+        o.x = E::pack(acc.x * inv, acc.y * inv);
+        o.y = E::pack(acc.z * inv, acc.w * inv);
+        *reinterpret_cast<uint2*>(a.O + row * kD + lane * 4) = o;
+        if (a.lse && lane == 0) a.lse[row] = L == 0.f ? kNegInf : M + log2f(L);
+        __syncwarp();
+    }
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], unsigned addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], unsigned addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t movt(uint32_t x) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(x));
+    return r;
+}
+
+// A place in the walk over the CTA's granules: unit (b, h), granule x of its
+// sequence.
+struct Cursor {
+    int b, h, x, hi;  // x in [span.first(), hi)
+    Span s;
+};
+
+template <class E, int NT, bool GATHER>
+__global__ void __launch_bounds__(kPgThreads, kPgCtasPerSm)
+paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const PgArgs a) {
+    using Cfg = PgCfg<NT>;
+    extern __shared__ __align__(1024) unsigned char pg_smem[];
+    uint64_t* s_full = reinterpret_cast<uint64_t*>(pg_smem + Cfg::kBars);  // per warp and stage
+    long long* s_scan = reinterpret_cast<long long*>(pg_smem + Cfg::kScan);
+    long long& s_base = s_scan[kPgWarps];
+    int& s_b = reinterpret_cast<int*>(s_scan + kPgWarps + 1)[0];
+    int& s_last = reinterpret_cast<int*>(s_scan + kPgWarps + 1)[1];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
+    unsigned char* ringp = pg_smem + warp * Cfg::kStages * kPgStage;
+    const unsigned ring = su32(ringp);
+    float* merge = reinterpret_cast<float*>(pg_smem + Cfg::kMerge);
+    if (!GATHER && lane == 0) {
+        for (int i = 0; i < Cfg::kStages; ++i) mbar_init(su32(&s_full[warp * Cfg::kStages + i]), 1);
+        mbar_init_fence();
+    }
+    griddep_wait();
+
+    // ---- the CTA's share: granules [g0, g1) of all units' laid end to end
+    const int B = a.c.B, Hkv = a.c.Hkv;
+    auto block_sum = [&](long long v, long long* before) {  // sum over the CTA; *before: of the lower threads
+        long long inc = v;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const long long o = __shfl_up_sync(0xffffffffu, inc, m);
+            if (lane >= m) inc += o;
+        }
+        __syncthreads();
+        if (lane == 31) s_scan[warp] = inc;
+        __syncthreads();
+        long long pre = 0, tot = 0;
+        for (int w = 0; w < kPgWarps; ++w) {
+            if (w < warp) pre += s_scan[w];
+            tot += s_scan[w];
+        }
+        *before = pre + inc - v;
+        return tot;
+    };
+    long long total = 0, before;
+    for (int b0 = 0; b0 < B; b0 += kPgThreads) {
+        const int b = b0 + tid;
+        const long long v = b < B ? (long long)span_of<GATHER>(a, b, cta == 0).granules() * Hkv : 0;
+        total += block_sum(v, &before);
+    }
+    const long long nc = min((long long)gridDim.x, total);  // CTAs with work: a granule each at least
+    const long long g0 = cta < nc ? total * cta / nc : 0, g1 = cta < nc ? total * (cta + 1) / nc : 0;
+    if (tid == 0) s_b = -1;
+    long long run = 0;
+    for (int b0 = 0; b0 < B && g0 < g1; b0 += kPgThreads) {  // which sequence holds granule g0
+        const int b = b0 + tid;
+        const long long v = b < B ? (long long)span_of<GATHER>(a, b, false).granules() * Hkv : 0;
+        const long long t = block_sum(v, &before);
+        if (v > 0 && run + before <= g0 && g0 < run + before + v) {
+            s_b = b;
+            s_base = run + before;
+        }
+        run += t;
+        if (run > g0) break;
+    }
+    __syncthreads();
+
+    const long long prow = (long long)B * a.Hq * kPartFloats;
+    if (g0 < g1) {
+        auto enter = [&](Cursor& c) {  // c.b is set: the span, its first granule
+            c.s = span_of<GATHER>(a, c.b, false);
+            c.x = c.s.first();
+            c.hi = c.x + c.s.granules();
+        };
+        auto advance = [&](Cursor& c) {  // to the next granule (the caller knows there is one)
+            if (++c.x < c.hi) return false;
+            if (++c.h == Hkv) {
+                c.h = 0;
+                do {
+                    ++c.b;
+                    enter(c);
+                } while (c.hi == c.x);
+            } else {
+                c.x = c.s.first();
+            }
+            return true;
+        };
+        Cursor at;  // of the consumer
+        at.b = s_b;
+        enter(at);
+        {
+            const long long off = g0 - s_base;
+            const int n = at.s.granules();
+            at.h = (int)(off / n);
+            at.x += (int)(off - (long long)at.h * n);
+        }
+        Cursor ld = at;  // of the loads
+        const int total_g = (int)(g1 - g0);
+
+        // ---- the loads.  Every row: lane i keeps the page of this warp's tile of
+        // granule pg_x + i.  A tile that is not there (no row of the sequence in
+        // it, or a bad page) is not loaded; `there` says so per stage.
+        int pages = -1, pg_x = 0;
+        bool fresh = true;  // `pages` is of another unit
+        unsigned there = 0, pending = 0, phase = 0;  // bits of the stages: holds a tile; on its way; barrier's phase
+        bool dead = false;                           // a wait gave up: this warp loads and adds no more
+        uint64_t pol = evict_first_policy();
+        auto issue = [&](int slot) {
+            const int r0 = ld.x * kPgGranule + warp * kPageRows;  // the tile's first row (or list entry)
+            bool ok = r0 < ld.s.hi && r0 + kPageRows > ld.s.lo;
+            if constexpr (!GATHER) {
+                if (fresh || ld.x - pg_x >= 32) {
+                    pg_x = ld.x;
+                    const int r = (ld.x + lane) * kPgGranule + warp * kPageRows;
+                    pages = -1;
+                    if (ld.x + lane < ld.hi && r < ld.s.hi) {
+                        pages = a.c.table[(long long)ld.b * a.c.width + r / a.c.page_size];
+                        if ((pages < 0 || pages >= a.c.num_pages) && r + kPageRows > ld.s.lo) {
+                            atomicOr(a.flag, kFlagBounds);
+                            pages = -1;
+                        }
+                    }
+                    fresh = false;
+                }
+                const int page = __shfl_sync(0xffffffffu, pages, ld.x - pg_x);
+                ok = ok && page >= 0;
+                if (ok && lane == 0) {
+                    const unsigned bar = su32(&s_full[warp * Cfg::kStages + slot]), dst = ring + slot * kPgStage;
+                    const int r = r0 % a.c.page_size;
+                    mbar_arrive_tx(bar, kPgStage);
+                    tma_4d(dst, &kmap, 0, r, ld.h, page, bar, pol);
+                    tma_4d(dst + kPgHalf, &kmap, 64, r, ld.h, page, bar, pol);
+                    tma_4d(dst + 2 * kPgHalf, &vmap, 0, r, ld.h, page, bar, pol);
+                    tma_4d(dst + 3 * kPgHalf, &vmap, 64, r, ld.h, page, bar, pol);
+                }
+                if (ok) pending |= 1u << slot;
+            } else {
+                // lane i < 16 finds entry i's row; a missing or bad one is filled with zeros and masked
+                long long off = -1;
+                if (ok && lane < kPageRows && r0 + lane < ld.s.hi) {
+                    const int e = a.idx[((long long)ld.b * Hkv + ld.h) * a.k_max + r0 + lane];
+                    const int len = min(max(a.lens[ld.b], 0), a.c.rows_cap());
+                    if (e >= len) {
+                        atomicOr(a.flag, kFlagBounds);
+                    } else if (e >= 0) {
+                        const int pg = e / a.c.page_size, page = a.c.table[(long long)ld.b * a.c.width + pg];
+                        if (page < 0 || page >= a.c.num_pages)
+                            atomicOr(a.flag, kFlagBounds);
+                        else
+                            off = page * a.c.page_stride + ld.h * a.c.head_stride +
+                                  (long long)(e - pg * a.c.page_size) * a.c.row_stride;
+                    }
+                }
+                const unsigned valid = __ballot_sync(0xffffffffu, off >= 0);
+                ok = valid != 0;
+                if (ok) {
+                    const unsigned dst = ring + slot * kPgStage;
+                    const int ch = lane & 15;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int r = (lane >> 4) + 2 * j;
+                        const long long o = __shfl_sync(0xffffffffu, off, r);
+                        const unsigned d = dst + (ch >> 3) * kPgHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+                        const int n = o >= 0 ? 16 : 0;
+                        const long long e = (o >= 0 ? o : 0) + ch * 8;
+                        cp_async16(d, static_cast<const uint16_t*>(a.c.K) + e, n);
+                        cp_async16(d + 2 * kPgHalf, static_cast<const uint16_t*>(a.c.V) + e, n);
+                    }
+                    // the rows' mask, for the consumer of this stage
+                    if (lane == 0) s_full[warp * Cfg::kStages + slot] = valid;
+                }
+                cp_async_commit();
+            }
+            there = (there & ~(1u << slot)) | ((ok ? 1u : 0u) << slot);
+        };
+        int issued = 0;
+        auto issue_next = [&](int slot) {
+            if (issued < total_g && !dead) {
+                issue(slot);
+                if (++issued < total_g && advance(ld)) fresh = true;
+            } else if (GATHER) {
+                cp_async_commit();
+            }
+        };
+        __syncwarp();
+        for (int i = 0; i < Cfg::kStages; ++i) issue_next(i);
+
+        // ---- the products
+        uint32_t qf[NT][8][2];
+        float acc[NT][8][4], m[NT][2], l[NT][2];
+        bool open = false;  // a unit is being summed
+        int seg0 = 0;       // its first granule here
+        for (int i = 0, slot = 0; i < total_g; ++i, slot = slot + 1 == Cfg::kStages ? 0 : slot + 1) {
+            if (!open) {
+                open = true;
+                seg0 = at.x;
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const int head = t * 8 + (lane >> 2);
+                    const uint16_t* qp = a.Q + ((long long)at.b * a.Hq + at.h * a.G + head) * kD + (lane & 3) * 2;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        qf[t][k][0] = head < a.G ? *reinterpret_cast<const uint32_t*>(qp + k * 16) : 0u;
+                        qf[t][k][1] = head < a.G ? *reinterpret_cast<const uint32_t*>(qp + k * 16 + 8) : 0u;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) acc[t][k][0] = acc[t][k][1] = acc[t][k][2] = acc[t][k][3] = 0.f;
+                    m[t][0] = m[t][1] = kNegInf;
+                    l[t][0] = l[t][1] = 0.f;
+                }
+            }
+            if constexpr (GATHER) {
+                cp_async_wait<Cfg::kStages - 1>();
+                __syncwarp();
+            }
+            bool here = !dead && (there >> slot & 1u);
+            if (!GATHER && here) {
+                dead = !__all_sync(0xffffffffu, mbar_wait(su32(&s_full[warp * Cfg::kStages + slot]), phase >> slot & 1u, a.flag));
+                here = !dead;
+            }
+            if (here) {
+                const unsigned st = ring + slot * kPgStage;
+                unsigned valid;  // a bit per row of the tile
+                if constexpr (GATHER) {
+                    valid = (unsigned)s_full[warp * Cfg::kStages + slot];
+                } else {
+                    phase ^= 1u << slot;
+                    pending &= ~(1u << slot);
+                    const int r0 = at.x * kPgGranule + warp * kPageRows;
+                    valid = 0xffffu;
+                    if (r0 + kPageRows > at.s.hi) valid &= 0xffffu >> (r0 + kPageRows - at.s.hi);
+                    if (r0 < at.s.lo) valid &= 0xffffu << (at.s.lo - r0);
+                    valid &= 0xffffu;
+                    if (valid != 0xffffu) {
+                        unsigned char* vp = ringp + slot * kPgStage + 2 * kPgHalf;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const int r = (lane >> 4) + 2 * j;
+                            if (!(valid >> r & 1u))
+                                *reinterpret_cast<uint4*>(vp + (lane >> 3 & 1) * kPgHalf + r * 128 + (lane & 7) * 16) =
+                                    make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async();  // before the next copy into this stage
+                        __syncwarp();
+                    }
+                }
+                float s[NT][4];
+#pragma unroll
+                for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+                const int fr = lane & 15, fc = lane >> 4;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    uint32_t kf[4];
+                    ldsm4(kf, st + (k >> 2) * kPgHalf + fr * 128 + ((((k & 3) * 2 + fc) ^ (fr & 7)) << 4));
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) E::mma(s[t], kf, qf[t][k][0], qf[t][k][1]);
+                }
+                const int row = lane >> 2;
+                const bool v0 = valid >> row & 1u, v1 = valid >> (row + 8) & 1u;
+                bool up = false;
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[t][j] = (j < 2 ? v0 : v1) ? s[t][j] * a.scale_log2 : kNegInf;
+                    up |= fmaxf(s[t][0], s[t][2]) > m[t][0] || fmaxf(s[t][1], s[t][3]) > m[t][1];
+                }
+                if (__any_sync(0xffffffffu, up)) {  // a larger maximum: rescale what there is
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            float x = fmaxf(s[t][j], s[t][j + 2]);
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                            x = fmaxf(x, m[t][j]);
+                            const float f = x == kNegInf ? 1.f : exp2f(m[t][j] - x);
+                            m[t][j] = x;
+                            l[t][j] *= f;
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) acc[t][k][j] *= f, acc[t][k][j + 2] *= f;
+                        }
+                    }
+                }
+                uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    // (no row so far: the scores are -inf and the weights 0)
+                    const float ms[2] = {m[t][0] == kNegInf ? 0.f : m[t][0], m[t][1] == kNegInf ? 0.f : m[t][1]};
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        // j = 0: rows 0-7, j = 1: rows 8-15; two heads each
+                        const float p0 = exp2f(s[t][2 * j] - ms[0]), p1 = exp2f(s[t][2 * j + 1] - ms[1]);
+                        l[t][0] += p0;
+                        l[t][1] += p1;
+                        const uint32_t hi = E::pack(p0, p1);
+                        ph[t][j] = movt(hi);
+                        pl[t][j] = movt(E::pack(p0 - E::lo(hi), p1 - E::hi(hi)));
+                    }
+                }
+                // V^T fragments: rows of the stage are tokens, 16 dims an m-tile
+                const int vr = (lane & 7) + (lane >> 4) * 8, vc = lane >> 3 & 1;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    uint32_t vf[4];
+                    ldsm4t(vf, st + (2 + (k >> 2)) * kPgHalf + vr * 128 + ((((k & 3) * 2 + vc) ^ (vr & 7)) << 4));
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        E::mma(acc[t][k], vf, ph[t][0], ph[t][1]);
+                        E::mma(acc[t][k], vf, pl[t][0], pl[t][1]);
+                    }
+                }
+            }
+            __syncwarp();
+            issue_next(slot);
+
+            // ---- the end of the unit here
+            const Cursor cur = at;
+            const bool last = i + 1 == total_g;
+            if (!last && !advance(at)) continue;
+            open = false;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float x = l[t][j];
+                    x += __shfl_xor_sync(0xffffffffu, x, 4);
+                    x += __shfl_xor_sync(0xffffffffu, x, 8);
+                    x += __shfl_xor_sync(0xffffffffu, x, 16);
+                    const int head = t * 8 + (lane & 3) * 2 + j;
+                    float* w = merge + (warp * Cfg::kHeads + head) * kPartFloats;
+                    if (lane < 4) {
+                        w[kD] = m[t][j];
+                        w[kD + 1] = x;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        w[k * 16 + (lane >> 2)] = acc[t][k][j];
+                        w[k * 16 + (lane >> 2) + 8] = acc[t][k][j + 2];
+                    }
+                }
+            }
+            __syncthreads();
+            // the unit's granules laid end to end: [u0, u1)
+            const bool starts = seg0 == cur.s.first(), ends = cur.x + 1 == cur.hi;
+            const bool whole = starts && ends && a.pre.splits == 0;
+            const long long gend = g0 + i + 1, u1 = gend + (cur.hi - cur.x - 1), u0 = u1 - cur.s.granules();
+            const long long c0 = ((u0 + 1) * nc - 1) / total, c1 = (u1 * nc - 1) / total;  // its CTAs
+            float* mine = a.pieces + (2LL * cta + (u0 > g0 ? 1 : 0)) * a.G * kPartFloats;
+            for (int g = warp; g < a.G; g += kPgWarps) {
+                float M = kNegInf, L = 0.f, f[kPgWarps];
+                const float* w = merge + g * kPartFloats;
+                constexpr int S = Cfg::kHeads * kPartFloats;
+#pragma unroll
+                for (int k = 0; k < kPgWarps; ++k) M = fmaxf(M, w[k * S + kD]);
+#pragma unroll
+                for (int k = 0; k < kPgWarps; ++k) {
+                    const float mk = w[k * S + kD];
+                    f[k] = mk == kNegInf ? 0.f : exp2f(mk - M);
+                    L += (mk == kNegInf ? w[k * S + kD + 1] * 0.f : f[k] * w[k * S + kD + 1]);
+                }
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < kPgWarps; ++k) {
+                    const float4 v = *(reinterpret_cast<const float4*>(w + k * S) + lane);
+                    o.x = fmaf(f[k], v.x, o.x), o.y = fmaf(f[k], v.y, o.y);
+                    o.z = fmaf(f[k], v.z, o.z), o.w = fmaf(f[k], v.w, o.w);
+                }
+                if (whole) {
+                    const float inv = L == 0.f ? 0.f : 1.0f / L;
+                    const long long orow = (long long)cur.b * a.Hq + cur.h * a.G + g;
+                    uint2 ov;
+                    ov.x = E::pack(o.x * inv, o.y * inv);
+                    ov.y = E::pack(o.z * inv, o.w * inv);
+                    *reinterpret_cast<uint2*>(a.O + orow * kD + lane * 4) = ov;
+                    if (a.lse && lane == 0) a.lse[orow] = L == 0.f ? kNegInf : M + log2f(L);
+                } else {
+                    // (a unit that one CTA holds whole, over a prefix, takes a piece, too:
+                    // only this CTA reads it, so the first of its two slots will do)
+                    float* p = mine + g * kPartFloats;
+                    __stcg(reinterpret_cast<float4*>(p) + lane, o);
+                    if (lane == 0) {
+                        __stcg(p + kD, M);
+                        __stcg(p + kD + 1, L);
+                    }
+                }
+            }
+            if (!whole) {
+                bool join = true;
+                if (c0 != c1) {
+                    __threadfence();
+                    __syncthreads();
+                    if (tid == 0) {
+                        const unsigned n = (unsigned)(c1 - c0 + 1);
+                        unsigned* cnt = a.counters + (long long)cur.b * Hkv + cur.h;
+                        const unsigned old = atomicAdd(cnt, 1u);
+                        if (old + 1 == n) *cnt = 0u;
+                        s_last = old + 1 == n;
+                    }
+                    __syncthreads();
+                    join = s_last != 0;
+                    __threadfence();
+                } else {
+                    __syncthreads();
+                }
+                if (join) {
+                    const bool pre = a.pre.splits > 0 && cur.s.lo > 0;
+                    const float* p0 = pre ? a.pre.parts + ((long long)cur.b * a.Hq + cur.h * a.G) * kPartFloats : nullptr;
+                    auto slot_of = [&](int k) -> const float* {
+                        const long long c = c0 + k;
+                        const bool second = k == 0 && u0 > total * c / nc;
+                        return a.pieces + (2 * c + (second ? 1 : 0)) * a.G * kPartFloats;
+                    };
+                    finish<E>(a, cur.b, cur.h, pre ? a.pre.splits : 0, p0, prow, (int)(c1 - c0 + 1), slot_of, merge);
+                }
+            }
+            __syncthreads();  // the merge buffer is free again
+        }
+        if (GATHER) cp_async_wait<0>();
+        // (only after a wait gave up) nothing lands after the CTA has gone
+        for (int i = 0; i < Cfg::kStages; ++i)
+            if (pending >> i & 1u) mbar_wait(su32(&s_full[warp * Cfg::kStages + i]), phase >> i & 1u, nullptr);
+    }
+
+    // ---- sequences without a row of their own: O from the prefix's partials, or zero
+    for (int b = cta; b < B; b += gridDim.x) {
+        if (span_of<GATHER>(a, b, false).granules() > 0) continue;
+        const bool whole = a.pre.splits > 0 && a.lens[b] >= a.pre.prefix_len;
+        for (int h = 0; h < Hkv; ++h) {
+            const float* p0 = whole ? a.pre.parts + ((long long)b * a.Hq + h * a.G) * kPartFloats : nullptr;
+            finish<E>(a, b, h, whole ? a.pre.splits : 0, p0, prow, 0, [](int) { return (const float*)nullptr; }, merge);
+            __syncthreads();
+        }
+    }
+    griddep_launch();
+}
+
+template <class E, int NT, bool GATHER>
+static cudaError_t paged_launch(int grid, const CUtensorMap& km, const CUtensorMap& vm, const PgArgs& a, cudaStream_t st) {
+    static std::atomic<unsigned long long> done{0};
+    const cudaError_t e0 = smem_opt_in((const void*)paged_attn_kernel<E, NT, GATHER>, PgCfg<NT>::kSmem, &done);
+    if (e0 != cudaSuccess) return e0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kPgThreads);
+    cfg.dynamicSmemBytes = PgCfg<NT>::kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1] = {pdl_attr()};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_attn_kernel<E, NT, GATHER>, km, vm, a);
+    note_launch();
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <class E>
+static cudaError_t paged_pick(int grid, const CUtensorMap& km, const CUtensorMap& vm, const PgArgs& a, cudaStream_t st) {
+    if (a.idx) return a.G <= 8 ? paged_launch<E, 1, true>(grid, km, vm, a, st) : paged_launch<E, 2, true>(grid, km, vm, a, st);
+    return a.G <= 8 ? paged_launch<E, 1, false>(grid, km, vm, a, st) : paged_launch<E, 2, false>(grid, km, vm, a, st);
+}
+
+cudaError_t launch_paged_attn(const Pages& c, const void* Q, int Hq, const int32_t* lens, const int32_t* idx,
+                              const int32_t* kreq, int k_max, float scale, void* O, float* lse, float* pieces,
+                              unsigned* counters, const PrefixParts& pre, unsigned* flag, cudaStream_t st) {
+    if (c.B == 0) return cudaSuccess;
+    PgArgs a;
+    a.c = c;
+    a.Q = static_cast<const uint16_t*>(Q);
+    a.Hq = Hq;
+    a.G = Hq / c.Hkv;
+    a.lens = lens;
+    a.idx = idx;
+    a.kreq = kreq;
+    a.k_max = k_max;
+    a.scale_log2 = scale * kLog2e;
+    a.O = static_cast<uint16_t*>(O);
+    a.lse = lse;
+    a.pieces = pieces;
+    a.counters = counters;
+    a.pre = pre;
+    a.flag = flag;
+    CUtensorMap km = {}, vm = {};
+    if (!idx) {
+        cudaError_t e = page_map(&km, c, c.K, kPageRows);
+        if (e == cudaSuccess) e = page_map(&vm, c, c.V, kPageRows);
+        if (e != cudaSuccess) return e;
+    }
+    const int grid = paged_ctas();
+    return c.half ? paged_pick<F16>(grid, km, vm, a, st) : paged_pick<Bf16>(grid, km, vm, a, st);
+}
+
+}  // namespace tsa

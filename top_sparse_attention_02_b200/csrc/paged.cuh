@@ -1,0 +1,65 @@
+// paged.cuh -- device helpers of the paged-cache kernels: element types and the
+// warp's matrix instructions on them.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "paged.h"
+
+namespace tsa {
+
+constexpr int kPagedSms = 148;
+
+struct Bf16 {
+    static constexpr bool kHalf = false;
+    static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+        uint32_t r;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
+        return r;
+    }
+    static __device__ __forceinline__ float lo(uint32_t w) { return bf_lo(w); }
+    static __device__ __forceinline__ float hi(uint32_t w) { return bf_hi(w); }
+    static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};\n"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    }
+    static __device__ __forceinline__ void unpack8(const uint4& r, float (&f)[8]) {
+        f[0] = lo(r.x), f[1] = hi(r.x), f[2] = lo(r.y), f[3] = hi(r.y);
+        f[4] = lo(r.z), f[5] = hi(r.z), f[6] = lo(r.w), f[7] = hi(r.w);
+    }
+    static __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+        return make_uint4(pack(f[0], f[1]), pack(f[2], f[3]), pack(f[4], f[5]), pack(f[6], f[7]));
+    }
+    static __device__ __forceinline__ uint16_t one(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
+};
+
+struct F16 {
+    static constexpr bool kHalf = true;
+    static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+        uint32_t r;
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
+        return r;
+    }
+    static __device__ __forceinline__ float lo(uint32_t w) { return __half2float(__ushort_as_half((unsigned short)w)); }
+    static __device__ __forceinline__ float hi(uint32_t w) { return __half2float(__ushort_as_half((unsigned short)(w >> 16))); }
+    static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};\n"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    }
+    static __device__ __forceinline__ void unpack8(const uint4& r, float (&f)[8]) {
+        f[0] = lo(r.x), f[1] = hi(r.x), f[2] = lo(r.y), f[3] = hi(r.y);
+        f[4] = lo(r.z), f[5] = hi(r.z), f[6] = lo(r.w), f[7] = hi(r.w);
+    }
+    static __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+        return make_uint4(pack(f[0], f[1]), pack(f[2], f[3]), pack(f[4], f[5]), pack(f[6], f[7]));
+    }
+    static __device__ __forceinline__ uint16_t one(float x) { return __half_as_ushort(__float2half_rn(x)); }
+};
+
+}  // namespace tsa
