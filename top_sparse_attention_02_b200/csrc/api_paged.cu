@@ -148,18 +148,22 @@ tsa_status check_ws(const void* ws, size_t ws_bytes, size_t need) {
     return TSA_OK;
 }
 
-// [flag 256 B][a counter per unit, zero between calls][the CTAs' pieces]
+// [flag 256 B][a counter per unit, zero between calls][the CTAs' pieces][a shared prefix's partials]
 struct Layout {
-    size_t counters, pieces, total;
+    size_t counters, pieces, parts, total;
 };
 
-Layout layout(const tsa::Pages& c, int Hq) {
+Layout layout(const tsa::Pages& c, int Hq, int prefix_len) {
     Layout L;
     size_t off = kFlagBytes;
     L.counters = off;
     off += a256((size_t)c.B * c.Hkv * sizeof(unsigned));
     L.pieces = off;
     off += a256((size_t)2 * tsa::paged_ctas() * (Hq / c.Hkv) * tsa::kPartFloats * sizeof(float));
+    L.parts = off;
+    if (prefix_len > 0)
+        off += a256((size_t)tsa::prefix_max_splits(c.Hkv, c.B * (Hq / c.Hkv), prefix_len) * c.B * Hq * tsa::kPartFloats *
+                    sizeof(float));
     L.total = off;
     return L;
 }
@@ -184,14 +188,21 @@ tsa_status attn(const tsa_paged_attn_args* a, bool prefix, const char* what, voi
         if (!aligned16(a->Q) || !aligned16(a->O)) return fail(TSA_ERR_INVALID_ARG, "%s: Q and O must be 16-byte aligned", what);
         if (a->O == a->Q) return fail(TSA_ERR_INVALID_ARG, "%s: O must not be Q", what);
     }
-    const Layout L = layout(c, a->Hq);
+    const Layout L = layout(c, a->Hq, a->prefix_len);
     TSA_TRY(check_ws(a->ws, a->ws_bytes, L.total));
+    if (a->prefix_len > 1 << 30) return fail(TSA_ERR_UNSUPPORTED, "%s: prefix_len=%d above 2^30", what, a->prefix_len);
     char* w = static_cast<char*>(a->ws);
     unsigned* flag = static_cast<unsigned*>(a->ws);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    tsa::PrefixParts pre;
+    if (a->prefix_len > 0 && a->prefix_len <= c.rows_cap() && c.B > 0) {  // (else no sequence holds it)
+        const cudaError_t e = tsa::launch_prefix(c, a->Q, a->Hq, a->seq_lens, a->prefix_len, a->scale,
+                                                 reinterpret_cast<float*>(w + L.parts), &pre, flag, st);
+        if (e != cudaSuccess) return cuda_fail(e, "tsa_prefix_attn (shared prefix)");
+    }
     const cudaError_t e = tsa::launch_paged_attn(c, a->Q, a->Hq, a->seq_lens, a->idx, a->k_per_seq, a->k_max, a->scale,
                                                  a->O, a->lse, reinterpret_cast<float*>(w + L.pieces),
-                                                 reinterpret_cast<unsigned*>(w + L.counters), tsa::PrefixParts(), flag,
-                                                 static_cast<cudaStream_t>(stream));
+                                                 reinterpret_cast<unsigned*>(w + L.counters), pre, flag, st);
     if (e != cudaSuccess) return cuda_fail(e, what);
     return TSA_OK;
 }
@@ -266,7 +277,7 @@ size_t tsa_paged_workspace_size(const tsa_paged_cache* cache, int32_t Hq, int32_
         fail(TSA_ERR_INVALID_ARG, "tsa_paged_workspace_size: prefix_len must be >= 0 (got %d)", prefix_len);
         return 0;
     }
-    return layout(c, Hq).total;
+    return layout(c, Hq, prefix_len).total;
 }
 
 tsa_status tsa_paged_attn(const tsa_paged_attn_args* args, void* stream) { return attn(args, false, "tsa_paged_attn", stream); }

@@ -54,6 +54,11 @@ struct PrefixParts {
     int splits = 0, prefix_len = 0;
 };
 
+// the shared prefix's pass into parts [prefix_max_splits][B][Hq][kPartFloats]; fills *out for the paged attention after it
+int prefix_max_splits(int Hkv, int rows, int prefix_len);  // rows = B * Hq / Hkv; grows with prefix_len
+cudaError_t launch_prefix(const Pages& c, const void* Q, int Hq, const int32_t* lens, int prefix_len, float scale,
+                          float* parts, PrefixParts* out, unsigned* flag, cudaStream_t st);
+
 int paged_ctas();  // CTAs of the paged attention's grid (at most)
 cudaError_t launch_paged_attn(const Pages& c, const void* Q, int Hq, const int32_t* lens, const int32_t* idx,
                               const int32_t* kreq, int k_max, float scale, void* O, float* lse, float* pieces,

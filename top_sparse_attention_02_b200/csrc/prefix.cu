@@ -1,0 +1,522 @@
+// prefix.cu -- the pass over a prefix that a batch of sequences shares: for each
+// kv-head the queries of all sequences, B * g rows, against the prefix's keys and
+// values, read once for all of them.  Its partials (per split of the prefix: the
+// sums, maximum and weight of every row) are joined with each sequence's own rows
+// by the paged attention that follows (paged.cu).
+//
+// With R = B g rows a kv-head the pass does 512 R flop for each 512 bytes of a row of
+// K and V, so up to about 250 rows HBM bounds it and above the tensor cores do:
+// both contractions run on tcgen05, tiles of 128 query rows x 128 prefix rows.
+//
+// A CTA (one per SM, 12 warps) takes up to 256 rows of one kv-head over one split
+// of the prefix, as two streams of 128 rows that take turns on the tensor cores:
+// while one stream's softmax runs on its four warps (a row per thread), the other's
+// products are computed.
+//   warp 9   TMA producer: K and V tiles of 128 prefix rows (boxes of as many rows as
+//            a page allows, 128-byte swizzle) into a ring of 5 stages of 32 KB;
+//   warp 8   MMA issuer: S = Q K^T into TMEM (128 columns a stream), then
+//            O += P V with P read from TMEM and V as stored (the MN-major operand);
+//   warps 0-3, 4-7  softmax of stream 0, 1: S from TMEM, the running maximum, P =
+//            2^(S - m) in 16 bits over S's columns; l in fp32.  O is rescaled in
+//            TMEM only when the maximum has grown by more than 2^8 (the result is the
+//            same: all sums are relative to the maximum they were formed with).
+//   warps 10, 11 only make warps 8-11 a warpgroup that hands registers to the softmax
+//            (168 a thread at launch; 56 here and 224 there).
+// TMEM is full: 2 x (S 128 + O 128) columns.  When 128 rows or fewer are left for a
+// CTA, both streams take the same rows and every other tile, and are joined at the
+// end in shared memory.
+//
+// Sequences shorter than the prefix have rows here, too, which nobody reads: no row
+// needs a mask of its own.  The prefix's last tile may be partial: its columns past
+// the end become -inf and its V rows there are zeroed in shared memory.  A page out
+// of range is read as zeros (a box outside the tensor map) and its columns masked.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "paged.cuh"
+#include "tma.cuh"
+
+namespace tsa {
+
+constexpr int kPxThreads = 384;
+constexpr int kPxTile = 128;                  // query rows of a stream, prefix rows of a tile
+constexpr int kPxRows = 2 * kPxTile;          // query rows of a CTA
+constexpr int kPxHalf = kPxTile * 128;        // 64 elements of 128 rows: 16 KB
+constexpr int kPxStage = 2 * kPxHalf;         // 32 KB
+constexpr int kPxStages = 5;
+constexpr int kPxQ = 0;                       // Q of both streams, 64 KB
+constexpr int kPxRing = 2 * kPxStage;
+constexpr int kPxBars = kPxRing + kPxStages * kPxStage;
+constexpr int kPxSmem = kPxBars + 256;
+constexpr int kPxJoinStride = kD + 4;         // floats of a row handed from stream 1 to stream 0
+constexpr int kPxTmemCols = 512;
+static_assert(kPxTile * kPxJoinStride * 4 <= kPxStages * kPxStage, "the rows handed over fit the ring");
+
+struct PxArgs {
+    const uint16_t* Q;
+    const int32_t *lens, *table;
+    int B, Hq, Hkv, G, width, page_size, num_pages, prefix_len;
+    int box_log, groups, splits;  // rows of a TMA box: 16 << box_log
+    float scale_log2;
+    float* parts;  // [splits][B][Hq][kPartFloats]
+    unsigned* flag;
+};
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(unsigned bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void tm_ld32(uint32_t (&r)[32], uint32_t addr) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tm_st32(uint32_t addr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};\n" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+
+// Shared-memory operand of a tile stored as two halves of 64 elements (128-byte
+// rows, 128-byte swizzle): the descriptor's low word holds the address (in 16
+// bytes) and the leading offset, its high word the stride offset (8-row groups
+// 1024 B apart), the version and the swizzle.
+//   K-major (the contraction runs along the row): no leading offset; 16 elements on = 32 B.
+//   MN-major (it runs across the rows): 64-element blocks a half (16 KB) apart; 16 rows on = 2048 B.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_k(unsigned saddr) { return (saddr >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_mn(unsigned saddr) { return (saddr >> 4) | ((uint32_t)(kPxHalf >> 4) << 16); }
+
+// D (+)= A B, A from shared memory (a low descriptor word) or from TMEM
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 da, db;\n mov.b64 da, {%1, %4};\n mov.b64 db, {%2, %4};\n setp.ne.b32 p, %5, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(kDescHi), "r"((int)add)
+        : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 db;\n mov.b64 db, {%2, %4};\n setp.ne.b32 p, %5, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(kDescHi), "r"((int)add)
+        : "memory");
+}
+// instruction descriptor: D f32, A and B bf16 (1) or f16 (0), N and M 128; B MN-major for the second product
+template <class E>
+__device__ constexpr uint32_t px_idesc(bool b_mn) {
+    const uint32_t t = E::kHalf ? 0u : 1u;
+    return (1u << 4) | (t << 7) | (t << 10) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(kPxTile >> 3) << 17) |
+           ((uint32_t)(kPxTile >> 4) << 24);
+}
+
+template <class E>
+__global__ void __launch_bounds__(kPxThreads, 1)
+prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const PxArgs a) {
+    extern __shared__ __align__(1024) unsigned char px_smem[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(px_smem + kPxBars);
+    const unsigned bar0 = su32(bars);
+    auto full = [&](int i) { return bar0 + i * 8; };
+    auto empty = [&](int i) { return bar0 + (kPxStages + i) * 8; };
+    auto sfull = [&](int s) { return bar0 + (2 * kPxStages + s) * 8; };
+    auto pfull = [&](int s) { return bar0 + (2 * kPxStages + 2 + s) * 8; };
+    auto ofull = [&](int s) { return bar0 + (2 * kPxStages + 4 + s) * 8; };
+    const unsigned drain = bar0 + (2 * kPxStages + 6) * 8;
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 2 * kPxStages + 7);
+    const int box_log = 4 + a.box_log, box = 1 << box_log, chunks = kPxTile >> box_log;
+
+    griddep_wait();
+    // the sequence through whose table the prefix is read: the first that holds it whole
+    int src = -1;
+    for (int b0 = 0; b0 < a.B && src < 0; b0 += 32) {
+        const unsigned v = __ballot_sync(0xffffffffu, b0 + lane < a.B && a.lens[b0 + lane] >= a.prefix_len);
+        if (v) src = b0 + __ffs(v) - 1;
+    }
+    if (src < 0) return;  // nobody does: uniform, before any barrier or TMEM
+
+    const int grp = blockIdx.x % a.groups, h = blockIdx.x / a.groups % a.Hkv, split = blockIdx.x / (a.groups * a.Hkv);
+    const int nt_all = (a.prefix_len + kPxTile - 1) / kPxTile;
+    const int t0 = (int)((long long)nt_all * split / a.splits), nt = (int)((long long)nt_all * (split + 1) / a.splits) - t0;
+    const int R = a.B * a.G, row0 = grp * kPxRows;
+    const bool pair = R - row0 > kPxTile;  // two streams of rows; else two streams of tiles
+    const int32_t* table = a.table + (long long)src * a.width;
+    // the tiles of stream s: all of the split's, or every other one
+    auto count = [&](int s) { return pair ? nt : (nt - s + 1) >> 1; };
+    auto tile_of = [&](int s, int i) { return pair ? i : 2 * i + s; };  // (of this CTA's)
+
+    if (warp == 8) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(su32(s_tmem)),
+                     "r"(kPxTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+    } else if (warp == 9) {
+        if (lane == 0) {
+            for (int i = 0; i < 2 * kPxStages; ++i) mbar_init(bar0 + i * 8, 1);
+            for (int s = 0; s < 2; ++s) {
+                mbar_init(sfull(s), 1);
+                mbar_init(pfull(s), kPxTile);
+                mbar_init(ofull(s), 1);
+            }
+            mbar_init(drain, 1);
+            mbar_init_fence();
+        }
+    } else if (warp < 8) {  // Q: row r of stream s at half * 16 KB + r * 128 B, 16-byte chunks swizzled; rows past R are zeros
+        const int rows = pair ? kPxRows : kPxTile;
+        for (int i = tid; i < rows * 16; i += 256) {
+            const int r = i >> 4, c = i & 15, gr = row0 + r;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (gr < R) {
+                const int b = gr / a.G, j = gr - b * a.G;
+                v = *reinterpret_cast<const uint4*>(a.Q + ((long long)b * a.Hq + h * a.G + j) * kD + c * 8);
+            }
+            const int rr = r & (kPxTile - 1);
+            unsigned char* dst = px_smem + kPxQ + (r >> 7) * kPxStage + (c >> 3) * kPxHalf + rr * 128 + (((c & 7) ^ (rr & 7)) << 4);
+            *reinterpret_cast<uint4*>(dst) = v;
+        }
+        fence_proxy_async();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *s_tmem;
+    // TMEM columns: S of stream s at s * 128 (P over its first 64), O at 256 + s * 128
+    const unsigned smem0 = su32(px_smem);
+
+    if (warp >= 8) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;\n");
+      if (warp == 9) {
+        // ---- TMA producer: K of tile t at ring position 2t, V at 2t + 1
+        const int chunk = lane >> 1, half = lane & 1;
+        const bool mine = chunk < chunks;
+        const uint64_t pol = evict_first_policy();
+        auto page_of = [&](int t, int* row) {  // this lane's box of tile t0 + t
+            const int r = (t0 + t) * kPxTile + chunk * box, pg = r / a.page_size;
+            *row = r - pg * a.page_size;
+            if (!mine || t >= nt || r >= a.prefix_len) return a.num_pages;  // outside the map: zeros
+            int page = table[pg];
+            if (page < 0 || page >= a.num_pages) {
+                atomicOr(a.flag, kFlagBounds);
+                page = a.num_pages;
+            }
+            return page;
+        };
+        int pos = 0, row, page = page_of(0, &row);
+        bool ok = true;
+        for (int t = 0; t < nt && ok; ++t) {
+            int nrow;
+            const int npage = page_of(t + 1, &nrow);
+            for (int kv = 0; kv < 2 && ok; ++kv, ++pos) {
+                const int st = pos % kPxStages, use = pos / kPxStages;
+                if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(empty(st), (use - 1) & 1, a.flag));
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_tx(full(st), kPxStage);
+                __syncwarp();
+                if (mine) {
+                    const unsigned dst = smem0 + kPxRing + st * kPxStage + half * kPxHalf + chunk * box * 128;
+                    tma_4d(dst, kv ? &vmap : &kmap, half * 64, row, h, page, full(st), pol);
+                }
+            }
+            row = nrow;
+            page = npage;
+        }
+        // what was requested has landed before the CTA leaves (at once, unless a wait gave up)
+        for (int p = max(0, pos - kPxStages); p < pos; ++p) mbar_wait(full(p % kPxStages), (p / kPxStages) & 1, nullptr);
+        __syncwarp();
+      } else if (warp == 8) {
+        // ---- MMA issuer
+        if (lane == 0) {
+            bool ok = true;
+            auto stage = [&](int pos) { return smem0 + kPxRing + pos % kPxStages * kPxStage; };
+            auto loaded = [&](int pos) { return mbar_wait(full(pos % kPxStages), (pos / kPxStages) & 1, a.flag); };
+            auto product_s = [&](int s, int i) {
+                const int pos = 2 * tile_of(s, i);
+                if (!loaded(pos)) return false;
+                tc_fence_after();
+                const uint32_t q = desc_k(smem0 + kPxQ + (pair ? s : 0) * kPxStage), kt = desc_k(stage(pos));
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint32_t off = ((k >> 2) * kPxHalf + (k & 3) * 32) >> 4;
+                    tc_mma_ss(tmem + s * 128, q + off, kt + off, px_idesc<E>(false), k > 0);
+                }
+                tc_commit(sfull(s));
+                if (!pair || s == 1) tc_commit(empty(pos % kPxStages));
+                return true;
+            };
+            auto product_o = [&](int s, int i) {
+                const int pos = 2 * tile_of(s, i) + 1;
+                if (!mbar_wait(pfull(s), i & 1, a.flag) || !loaded(pos)) return false;
+                tc_fence_after();
+                const uint32_t vt = desc_mn(stage(pos));
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    tc_mma_ts(tmem + 256 + s * 128, tmem + s * 128 + k * 8, vt + k * (2048 >> 4), px_idesc<E>(true), i + k > 0);
+                if (!pair || s == 1) tc_commit(empty(pos % kPxStages));
+                if (i + 1 == count(s)) tc_commit(ofull(s));
+                return true;
+            };
+            for (int s = 0; s < 2 && ok; ++s)
+                if (count(s) > 0) ok = product_s(s, 0);
+            for (int i = 0; ok && i < count(0); ++i) {
+                for (int s = 0; s < 2 && ok; ++s) {
+                    if (i < count(s)) ok = product_o(s, i);
+                    // (S of the next tile replaces this tile's P: the tensor core takes its instructions in order)
+                    if (ok && i + 1 < count(s)) ok = product_s(s, i + 1);
+                }
+            }
+            // the last products have been computed before TMEM is freed: the softmax
+            // warps waited for them, unless a wait gave up
+            if (!ok) {
+                tc_commit(drain);
+                mbar_wait(drain, 0, nullptr);
+            }
+        }
+        __syncwarp();
+      }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;\n");
+        // ---- softmax of stream s: this thread's row
+        const int s = warp >> 2, q = warp & 3;
+        const int n = count(s);
+        const uint32_t ts = tmem + ((uint32_t)(q * 32) << 16) + s * 128, to = ts + 256;
+        float m = -INFINITY, l = 0.f;
+        bool ok = true;
+        for (int i = 0; i < n; ++i) {
+            const int t = t0 + tile_of(s, i);
+            // the tile's columns that are rows of the prefix: a bit per box, and those before the end
+            const int r = t * kPxTile + lane * box;
+            bool good = false;
+            if (lane < chunks && r < a.prefix_len) {
+                const int page = table[r / a.page_size];
+                good = page >= 0 && page < a.num_pages;
+            }
+            const unsigned valid = __ballot_sync(0xffffffffu, good);
+            const int nv = min(kPxTile, a.prefix_len - t * kPxTile);
+            ok = __all_sync(0xffffffffu, mbar_wait(sfull(s), i & 1, a.flag));
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t x[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tm_ld32(x[c], ts + c * 32);
+            tm_wait_ld();
+            if (valid != (0xffffffffu >> (32 - chunks)) || nv < kPxTile) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const int col = c * 32 + j;
+                        if (col >= nv || !(valid >> (col >> box_log) & 1u)) x[c][j] = 0xff800000u;  // -inf
+                    }
+            }
+            float mx = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int j = 0; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(x[c][j]));
+            mx *= a.scale_log2;
+            // rescale when some row's maximum has left the range that the sums were formed for
+            const bool grow = mx > m + 8.f || (m == -INFINITY && mx > m);
+            if (__any_sync(0xffffffffu, grow)) {
+                const float f = grow ? (m == -INFINITY ? 0.f : exp2f(m - mx)) : 1.f;
+                if (grow) m = mx;
+                l *= f;
+                if (i > 0) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t o[32];
+                        tm_ld32(o, to + c * 32);
+                        tm_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                        tm_st32(to + c * 32, o);
+                    }
+                }
+            }
+            const float ms = m == -INFINITY ? 0.f : -m;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t p[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    const float a0 = __uint_as_float(x[2 * c + (j >> 4)][(2 * j) & 31]);
+                    const float a1 = __uint_as_float(x[2 * c + (j >> 4)][(2 * j + 1) & 31]);
+                    const float p0 = exp2f(fmaf(a0, a.scale_log2, ms)), p1 = exp2f(fmaf(a1, a.scale_log2, ms));
+                    l += p0;
+                    l += p1;
+                    p[j] = E::pack(p0, p1);
+                }
+                tm_st32(ts + c * 32, p);
+            }
+            if (nv < kPxTile) {  // zero V's rows past the end (the boxes past it came as zeros)
+                const int pos = 2 * tile_of(s, i) + 1;
+                ok = __all_sync(0xffffffffu, mbar_wait(full(pos % kPxStages), (pos / kPxStages) & 1, a.flag));
+                if (!ok) break;
+                unsigned char* v = px_smem + kPxRing + pos % kPxStages * kPxStage;
+                const int end = min(kPxTile, (nv + box - 1) & -box);
+                for (int j = tid & 127; j < (end - nv) * 16; j += 128)
+                    *reinterpret_cast<uint4*>(v + (j >> 3 & 1) * kPxHalf + (nv + (j >> 4)) * 128 + (j & 7) * 16) =
+                        make_uint4(0, 0, 0, 0);
+                fence_proxy_async();
+            }
+            tm_wait_st();
+            tc_fence_before();
+            mbar_arrive(pfull(s));
+        }
+        if (ok && n > 0) ok = __all_sync(0xffffffffu, mbar_wait(ofull(s), 0, a.flag));
+        tc_fence_after();
+        float* join = reinterpret_cast<float*>(px_smem + kPxRing);
+        const int row = tid & 127;
+        if (!pair) {  // stream 1 hands its rows to stream 0
+            asm volatile("bar.sync 1, 256;\n" ::: "memory");  // no product reads the ring any more
+            if (s == 1 && ok) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t o[32];
+                    if (n > 0) {
+                        tm_ld32(o, to + c * 32);
+                        tm_wait_ld();
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4)
+                        *reinterpret_cast<uint4*>(join + row * kPxJoinStride + c * 32 + j) =
+                            n > 0 ? make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]) : make_uint4(0, 0, 0, 0);
+                }
+                join[row * kPxJoinStride + kD] = m;
+                join[row * kPxJoinStride + kD + 1] = l;
+            }
+            asm volatile("bar.sync 1, 256;\n" ::: "memory");
+        }
+        const int gr = row0 + (pair ? s * kPxTile : 0) + row;
+        if (ok && (pair || s == 0)) {
+            const int b = gr / a.G, j = gr - b * a.G;
+            float* out = a.parts + (((long long)split * a.B + b) * a.Hq + h * a.G + j) * kPartFloats;
+            float f0 = 1.f, f1 = 0.f;
+            const float* other = join + row * kPxJoinStride;
+            if (!pair) {
+                const float m1 = other[kD], l1 = other[kD + 1], M = fmaxf(m, m1);
+                f0 = m == -INFINITY ? 0.f : exp2f(m - M);
+                f1 = m1 == -INFINITY ? 0.f : exp2f(m1 - M);
+                l = (m == -INFINITY ? l : f0 * l) + (m1 == -INFINITY ? l1 : f1 * l1);
+                m = M;
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t o[32];
+                tm_ld32(o, to + c * 32);
+                tm_wait_ld();
+                if (gr < R) {
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4) {
+                        float4 v = make_float4(__uint_as_float(o[k]), __uint_as_float(o[k + 1]), __uint_as_float(o[k + 2]),
+                                               __uint_as_float(o[k + 3]));
+                        if (!pair) {
+                            const float4 w = *reinterpret_cast<const float4*>(other + c * 32 + k);
+                            v.x = f0 * v.x + f1 * w.x, v.y = f0 * v.y + f1 * w.y;
+                            v.z = f0 * v.z + f1 * w.z, v.w = f0 * v.w + f1 * w.w;
+                        }
+                        *reinterpret_cast<float4*>(out + c * 32 + k) = v;
+                    }
+                }
+            }
+            if (gr < R) {
+                out[kD] = m;
+                out[kD + 1] = l;
+            }
+        }
+    }
+    griddep_launch();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(kPxTmemCols) : "memory");
+    }
+}
+
+// Splits of the prefix: as many as make the fewest rounds of CTAs over the SMs, each
+// round as long as its tiles and about three tiles' time of set-up and end.
+static int px_groups(int R) { return (R + kPxRows - 1) / kPxRows; }
+int prefix_max_splits(int Hkv, int R, int prefix_len) {
+    const long long items = (long long)Hkv * px_groups(R), nt = ((long long)prefix_len + kPxTile - 1) / kPxTile;
+    return (int)std::min(nt, std::max(1LL, 2 * kPagedSms / std::max(1LL, items)));
+}
+static int px_splits(int Hkv, int R, int prefix_len) {
+    const long long items = (long long)Hkv * px_groups(R), nt = ((long long)prefix_len + kPxTile - 1) / kPxTile;
+    int best = 1;
+    long long cost = -1;
+    for (int s = 1; s <= prefix_max_splits(Hkv, R, prefix_len); ++s) {
+        const long long c = (items * s + kPagedSms - 1) / kPagedSms * ((nt + s - 1) / s + 3);
+        if (cost < 0 || c < cost) best = s, cost = c;
+    }
+    return best;
+}
+
+template <class E>
+static cudaError_t px_launch(int grid, const CUtensorMap& km, const CUtensorMap& vm, const PxArgs& a, cudaStream_t st) {
+    static std::atomic<unsigned long long> done{0};
+    cudaError_t e = smem_opt_in((const void*)prefix_kernel<E>, kPxSmem, &done);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kPxThreads);
+    cfg.dynamicSmemBytes = kPxSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1] = {pdl_attr()};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, prefix_kernel<E>, km, vm, a);
+    note_launch();
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_prefix(const Pages& c, const void* Q, int Hq, const int32_t* lens, int prefix_len, float scale,
+                          float* parts, PrefixParts* out, unsigned* flag, cudaStream_t st) {
+    PxArgs a;
+    a.Q = static_cast<const uint16_t*>(Q);
+    a.lens = lens;
+    a.table = c.table;
+    a.B = c.B;
+    a.Hq = Hq;
+    a.Hkv = c.Hkv;
+    a.G = Hq / c.Hkv;
+    a.width = c.width;
+    a.page_size = c.page_size;
+    a.num_pages = c.num_pages;
+    a.prefix_len = prefix_len;
+    a.box_log = 0;  // the largest power of two that divides the page, a tile at most
+    while ((kPageRows << a.box_log) < kPxTile && c.page_size % (kPageRows << (a.box_log + 1)) == 0) ++a.box_log;
+    a.groups = px_groups(c.B * a.G);
+    a.splits = px_splits(c.Hkv, c.B * a.G, prefix_len);
+    a.scale_log2 = scale * kLog2e;
+    a.parts = parts;
+    a.flag = flag;
+    CUtensorMap km, vm;
+    cudaError_t e = page_map(&km, c, c.K, kPageRows << a.box_log);
+    if (e == cudaSuccess) e = page_map(&vm, c, c.V, kPageRows << a.box_log);
+    if (e != cudaSuccess) return e;
+    out->parts = parts;
+    out->splits = a.splits;
+    out->prefix_len = prefix_len;
+    const int grid = a.splits * c.Hkv * a.groups;
+    return c.half ? px_launch<F16>(grid, km, vm, a, st) : px_launch<Bf16>(grid, km, vm, a, st);
+}
+
+}  // namespace tsa
