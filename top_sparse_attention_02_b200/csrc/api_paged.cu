@@ -148,7 +148,8 @@ tsa_status check_ws(const void* ws, size_t ws_bytes, size_t need) {
     return TSA_OK;
 }
 
-// [flag 256 B][a counter per unit, zero between calls][the CTAs' pieces][a shared prefix's partials]
+// [flag 256 B][a counter per unit, zero between calls][the CTAs' pieces][a shared prefix's partials, and
+// those of the sequences' own rows]
 struct Layout {
     size_t counters, pieces, parts, total;
 };
@@ -162,8 +163,8 @@ Layout layout(const tsa::Pages& c, int Hq, int prefix_len) {
     off += a256((size_t)2 * tsa::paged_ctas() * (Hq / c.Hkv) * tsa::kPartFloats * sizeof(float));
     L.parts = off;
     if (prefix_len > 0)
-        off += a256((size_t)tsa::prefix_max_splits(c.Hkv, c.B * (Hq / c.Hkv), prefix_len) * c.B * Hq * tsa::kPartFloats *
-                    sizeof(float));
+        off += a256((size_t)(tsa::prefix_max_splits(c.Hkv, c.B * (Hq / c.Hkv), prefix_len) + 1) * c.B * Hq *
+                    tsa::kPartFloats * sizeof(float));
     L.total = off;
     return L;
 }

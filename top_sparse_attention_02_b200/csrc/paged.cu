@@ -83,6 +83,7 @@ struct PgArgs {
     float* pieces;       // [2 * gridDim.x][G][kPartFloats]
     unsigned* counters;  // [B * Hkv], zero between calls
     PrefixParts pre;
+    float* own;          // over a shared prefix: [B][Hq][kPartFloats], where this pass's partials go
     unsigned* flag;
 };
 
@@ -110,53 +111,65 @@ __device__ __forceinline__ Span span_of(const PgArgs& a, int b, bool report) {
     return s;
 }
 
-// Join parts of one (b, kv-head): n0 of them `part0` apart from `p0` (the prefix's
-// splits), n1 of them listed by slot(i) (the CTAs' pieces), each [G][kPartFloats]
-// with M and L after the 128 sums; write O and lse.  All threads of the CTA.
-template <class E, class Slot>
-__device__ void finish(const PgArgs& a, int b, int h, int n0, const float* p0, long long part0, int n1, Slot slot,
-                       float* wts) {
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = n0 + n1;
-    auto part = [&](int i) { return i < n0 ? p0 + i * part0 : slot(i - n0); };
-    for (int g = warp; g < a.G; g += kPgWarps) {
-        float M = kNegInf;
-        for (int i = lane; i < n; i += 32) {
-            const float* p = part(i) + g * kPartFloats;
-            if (__ldcg(p + kD + 1) > 0.f) M = fmaxf(M, __ldcg(p + kD));
+// A row's result out of its sums acc (4 of 128 a lane), maximum M and weight L: into O
+// and lse, or (over a shared prefix) as one more partial of the row.
+template <class E>
+__device__ __forceinline__ void put_row(const PgArgs& a, long long row, float4 acc, float M, float L, int lane) {
+    if (a.own) {
+        float* p = a.own + row * kPartFloats;
+        __stcg(reinterpret_cast<float4*>(p) + lane, acc);
+        if (lane == 0) {
+            __stcg(p + kD, M);
+            __stcg(p + kD + 1, L);
         }
-#pragma unroll
-        for (int m = 16; m; m >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
-        float L = 0.f;
-        bool bad = false;  // a NaN sum: the result is NaN, as the softmax's is
-        for (int i = lane; i < n; i += 32) {
-            const float* p = part(i) + g * kPartFloats;
-            const float l = __ldcg(p + kD + 1), w = l > 0.f ? exp2f(__ldcg(p + kD) - M) : 0.f;
-            bad |= l != l;
-            wts[g * n + i] = w;
-            L += w * l;
-        }
-#pragma unroll
-        for (int m = 16; m; m >>= 1) L += __shfl_xor_sync(0xffffffffu, L, m);
-        if (__any_sync(0xffffffffu, bad)) L = NAN;
-        __syncwarp();
-        const float inv = L == 0.f ? 0.f : 1.0f / L;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-            const float w = wts[g * n + i];
-            if (w == 0.f) continue;  // (a part without a row holds no sums)
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(part(i) + g * kPartFloats) + lane);
-            acc.x = fmaf(w, v.x, acc.x), acc.y = fmaf(w, v.y, acc.y);
-            acc.z = fmaf(w, v.z, acc.z), acc.w = fmaf(w, v.w, acc.w);
-        }
-        const long long row = (long long)b * a.Hq + h * a.G + g;
-        uint2 o;
-        o.x = E::pack(acc.x * inv, acc.y * inv);
-        o.y = E::pack(acc.z * inv, acc.w * inv);
-        *reinterpret_cast<uint2*>(a.O + row * kD + lane * 4) = o;
-        if (a.lse && lane == 0) a.lse[row] = L == 0.f ? kNegInf : M + log2f(L);
-        __syncwarp();
+        return;
     }
+    const float inv = L == 0.f ? 0.f : 1.0f / L;
+    uint2 o;
+    o.x = E::pack(acc.x * inv, acc.y * inv);
+    o.y = E::pack(acc.z * inv, acc.w * inv);
+    *reinterpret_cast<uint2*>(a.O + row * kD + lane * 4) = o;
+    if (a.lse && lane == 0) a.lse[row] = L == 0.f ? kNegInf : M + log2f(L);
+}
+
+// Join n partials of one row, part(i) for i < n, each kPartFloats with M and L after
+// its 128 sums: this lane's 4 sums relative to *M, and the weight *L.  All lanes of
+// the warp; wts holds n floats.
+template <class Part>
+__device__ __forceinline__ float4 join_row(int n, Part part, float* wts, int lane, float* M_out, float* L_out) {
+    float M = kNegInf;
+    for (int i = lane; i < n; i += 32) {
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(part(i) + kD));
+        if (ml.y > 0.f) M = fmaxf(M, ml.x);
+    }
+#pragma unroll
+    for (int m = 16; m; m >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
+    float L = 0.f;
+    bool bad = false;  // a NaN weight: the result is NaN, as the softmax's is
+    for (int i = lane; i < n; i += 32) {
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(part(i) + kD));
+        const float w = ml.y > 0.f ? exp2f(ml.x - M) : 0.f;
+        bad |= ml.y != ml.y;
+        wts[i] = w;
+        L += w * ml.y;
+    }
+#pragma unroll
+    for (int m = 16; m; m >>= 1) L += __shfl_xor_sync(0xffffffffu, L, m);
+    if (__any_sync(0xffffffffu, bad)) L = NAN;
+    __syncwarp();
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+        const float w = wts[i];
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(part(i)) + lane);
+        if (w == 0.f) continue;  // (a part without a row may hold anything)
+        acc.x = fmaf(w, v.x, acc.x), acc.y = fmaf(w, v.y, acc.y);
+        acc.z = fmaf(w, v.z, acc.z), acc.w = fmaf(w, v.w, acc.w);
+    }
+    __syncwarp();
+    *M_out = M;
+    *L_out = L;
+    return acc;
 }
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], unsigned addr) {
@@ -202,7 +215,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         for (int i = 0; i < Cfg::kStages; ++i) mbar_init(su32(&s_full[warp * Cfg::kStages + i]), 1);
         mbar_init_fence();
     }
-    griddep_wait();
+    // Over a shared prefix the kernel before this one is the prefix's pass, of which
+    // nothing is read here, and which has waited for the kernel before it.
+    if (a.pre.splits == 0) griddep_wait();
 
     // ---- the CTA's share: granules [g0, g1) of all units' laid end to end
     const int B = a.c.B, Hkv = a.c.Hkv;
@@ -247,7 +262,6 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     }
     __syncthreads();
 
-    const long long prow = (long long)B * a.Hq * kPartFloats;
     if (g0 < g1) {
         auto enter = [&](Cursor& c) {  // c.b is set: the span, its first granule
             c.s = span_of<GATHER>(a, c.b, false);
@@ -524,8 +538,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             }
             __syncthreads();
             // the unit's granules laid end to end: [u0, u1)
-            const bool starts = seg0 == cur.s.first(), ends = cur.x + 1 == cur.hi;
-            const bool whole = starts && ends && a.pre.splits == 0;
+            const bool whole = seg0 == cur.s.first() && cur.x + 1 == cur.hi;
             const long long gend = g0 + i + 1, u1 = gend + (cur.hi - cur.x - 1), u0 = u1 - cur.s.granules();
             const long long c0 = ((u0 + 1) * nc - 1) / total, c1 = (u1 * nc - 1) / total;  // its CTAs
             float* mine = a.pieces + (2LL * cta + (u0 > g0 ? 1 : 0)) * a.G * kPartFloats;
@@ -549,16 +562,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                     o.z = fmaf(f[k], v.z, o.z), o.w = fmaf(f[k], v.w, o.w);
                 }
                 if (whole) {
-                    const float inv = L == 0.f ? 0.f : 1.0f / L;
-                    const long long orow = (long long)cur.b * a.Hq + cur.h * a.G + g;
-                    uint2 ov;
-                    ov.x = E::pack(o.x * inv, o.y * inv);
-                    ov.y = E::pack(o.z * inv, o.w * inv);
-                    *reinterpret_cast<uint2*>(a.O + orow * kD + lane * 4) = ov;
-                    if (a.lse && lane == 0) a.lse[orow] = L == 0.f ? kNegInf : M + log2f(L);
+                    put_row<E>(a, (long long)cur.b * a.Hq + cur.h * a.G + g, o, M, L, lane);
                 } else {
-                    // (a unit that one CTA holds whole, over a prefix, takes a piece, too:
-                    // only this CTA reads it, so the first of its two slots will do)
                     float* p = mine + g * kPartFloats;
                     __stcg(reinterpret_cast<float4*>(p) + lane, o);
                     if (lane == 0) {
@@ -568,32 +573,29 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                 }
             }
             if (!whole) {
-                bool join = true;
-                if (c0 != c1) {
-                    __threadfence();
-                    __syncthreads();
-                    if (tid == 0) {
-                        const unsigned n = (unsigned)(c1 - c0 + 1);
-                        unsigned* cnt = a.counters + (long long)cur.b * Hkv + cur.h;
-                        const unsigned old = atomicAdd(cnt, 1u);
-                        if (old + 1 == n) *cnt = 0u;
-                        s_last = old + 1 == n;
-                    }
-                    __syncthreads();
-                    join = s_last != 0;
-                    __threadfence();
-                } else {
-                    __syncthreads();
+                __threadfence();
+                __syncthreads();
+                if (tid == 0) {
+                    const unsigned n = (unsigned)(c1 - c0 + 1);
+                    unsigned* cnt = a.counters + (long long)cur.b * Hkv + cur.h;
+                    const unsigned old = atomicAdd(cnt, 1u);
+                    if (old + 1 == n) *cnt = 0u;
+                    s_last = old + 1 == n;
                 }
-                if (join) {
-                    const bool pre = a.pre.splits > 0 && cur.s.lo > 0;
-                    const float* p0 = pre ? a.pre.parts + ((long long)cur.b * a.Hq + cur.h * a.G) * kPartFloats : nullptr;
-                    auto slot_of = [&](int k) -> const float* {
-                        const long long c = c0 + k;
-                        const bool second = k == 0 && u0 > total * c / nc;
-                        return a.pieces + (2 * c + (second ? 1 : 0)) * a.G * kPartFloats;
-                    };
-                    finish<E>(a, cur.b, cur.h, pre ? a.pre.splits : 0, p0, prow, (int)(c1 - c0 + 1), slot_of, merge);
+                __syncthreads();
+                if (s_last) {
+                    __threadfence();
+                    const int n = (int)(c1 - c0 + 1);
+                    for (int g = warp; g < a.G; g += kPgWarps) {
+                        auto part = [&](int k) -> const float* {
+                            const long long c = c0 + k;
+                            const bool second = k == 0 && u0 > total * c / nc;
+                            return a.pieces + ((2 * c + (second ? 1 : 0)) * a.G + g) * kPartFloats;
+                        };
+                        float M, L;
+                        const float4 o = join_row(n, part, merge + g * n, lane, &M, &L);
+                        put_row<E>(a, (long long)cur.b * a.Hq + cur.h * a.G + g, o, M, L, lane);
+                    }
                 }
             }
             __syncthreads();  // the merge buffer is free again
@@ -604,17 +606,54 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             if (pending >> i & 1u) mbar_wait(su32(&s_full[warp * Cfg::kStages + i]), phase >> i & 1u, nullptr);
     }
 
-    // ---- sequences without a row of their own: O from the prefix's partials, or zero
+    // ---- sequences without a row (of their own)
     for (int b = cta; b < B; b += gridDim.x) {
         if (span_of<GATHER>(a, b, false).granules() > 0) continue;
-        const bool whole = a.pre.splits > 0 && a.lens[b] >= a.pre.prefix_len;
-        for (int h = 0; h < Hkv; ++h) {
-            const float* p0 = whole ? a.pre.parts + ((long long)b * a.Hq + h * a.G) * kPartFloats : nullptr;
-            finish<E>(a, b, h, whole ? a.pre.splits : 0, p0, prow, 0, [](int) { return (const float*)nullptr; }, merge);
-            __syncthreads();
-        }
+        for (int r = warp; r < a.Hq; r += kPgWarps)
+            put_row<E>(a, (long long)b * a.Hq + r, make_float4(0.f, 0.f, 0.f, 0.f), kNegInf, 0.f, lane);
+    }
+    if (a.pre.splits > 0) griddep_wait();  // the prefix's pass is over before this one counts as over
+    griddep_launch();
+}
+
+// Over a shared prefix: every row's partials (the prefix's splits, where the
+// sequence holds the prefix whole, and its own rows' one) into O and lse.  A warp a
+// row: the partials come out of L2.
+constexpr int kJoinThreads = 128;
+constexpr int kMaxParts = 2 * kPagedSms + 1;
+template <class E>
+__global__ void __launch_bounds__(kJoinThreads)
+prefix_join_kernel(const PgArgs a) {
+    __shared__ float wts[kJoinThreads / 32][kMaxParts];
+    griddep_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long row = (long long)blockIdx.x * (kJoinThreads / 32) + warp, rows = (long long)a.c.B * a.Hq;
+    if (row < rows) {
+        const int b = (int)(row / a.Hq);
+        const int n0 = a.lens[b] >= a.pre.prefix_len ? a.pre.splits : 0;
+        auto part = [&](int i) { return i < n0 ? a.pre.parts + (i * rows + row) * kPartFloats : a.own + row * kPartFloats; };
+        float M, L;
+        const float4 o = join_row(n0 + 1, part, wts[warp], lane, &M, &L);
+        PgArgs out = a;
+        out.own = nullptr;
+        put_row<E>(out, row, o, M, L, lane);
     }
     griddep_launch();
+}
+
+template <class E>
+static cudaError_t join_launch(const PgArgs& a, cudaStream_t st) {
+    const long long rows = (long long)a.c.B * a.Hq, per = kJoinThreads / 32;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((rows + per - 1) / per));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1] = {pdl_attr()};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, prefix_join_kernel<E>, a);
+    note_launch();
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <class E, int NT, bool GATHER>
@@ -660,6 +699,7 @@ cudaError_t launch_paged_attn(const Pages& c, const void* Q, int Hq, const int32
     a.pieces = pieces;
     a.counters = counters;
     a.pre = pre;
+    a.own = pre.splits > 0 ? pre.own : nullptr;
     a.flag = flag;
     CUtensorMap km = {}, vm = {};
     if (!idx) {
@@ -668,7 +708,9 @@ cudaError_t launch_paged_attn(const Pages& c, const void* Q, int Hq, const int32
         if (e != cudaSuccess) return e;
     }
     const int grid = paged_ctas();
-    return c.half ? paged_pick<F16>(grid, km, vm, a, st) : paged_pick<Bf16>(grid, km, vm, a, st);
+    const cudaError_t e = c.half ? paged_pick<F16>(grid, km, vm, a, st) : paged_pick<Bf16>(grid, km, vm, a, st);
+    if (e != cudaSuccess || pre.splits == 0) return e;
+    return c.half ? join_launch<F16>(a, st) : join_launch<Bf16>(a, st);
 }
 
 }  // namespace tsa

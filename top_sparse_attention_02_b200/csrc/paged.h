@@ -48,9 +48,11 @@ cudaError_t launch_paged_append(const Pages& c, const Heads& k, const Heads& v, 
                                 cudaStream_t st);
 
 // Partials of a shared prefix's pass: [splits][B][Hq][kPartFloats], counted only
-// for the sequences that hold the whole prefix (len >= prefix_len).
+// for the sequences that hold the whole prefix (len >= prefix_len); and room for
+// those of each sequence's own rows.
 struct PrefixParts {
-    const float* parts = nullptr;
+    float* parts = nullptr;
+    float* own = nullptr;  // [B][Hq][kPartFloats]
     int splits = 0, prefix_len = 0;
 };
 

@@ -145,6 +145,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     const int box_log = 4 + a.box_log, box = 1 << box_log, chunks = kPxTile >> box_log;
 
     griddep_wait();
+    griddep_launch();  // the pass over the sequences' own rows reads nothing of this one
     // the sequence through whose table the prefix is read: the first that holds it whole
     int src = -1;
     for (int b0 = 0; b0 < a.B && src < 0; b0 += 32) {
@@ -442,7 +443,6 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             }
         }
     }
-    griddep_launch();
     tc_fence_before();
     __syncthreads();
     if (warp == 8) {
@@ -513,6 +513,7 @@ cudaError_t launch_prefix(const Pages& c, const void* Q, int Hq, const int32_t* 
     if (e == cudaSuccess) e = page_map(&vm, c, c.V, kPageRows << a.box_log);
     if (e != cudaSuccess) return e;
     out->parts = parts;
+    out->own = parts + (size_t)a.splits * c.B * Hq * kPartFloats;
     out->splits = a.splits;
     out->prefix_len = prefix_len;
     const int grid = a.splits * c.Hkv * a.groups;
