@@ -334,19 +334,23 @@ def _tensor(t, what: str, dtype, shape, device, contiguous: bool = True):
 
 def _hold(a, device, *tensors):
     """The arguments keep their tensors alive and remember their device."""
-    a._tensors, a._device = tensors, device
+    a._tensors, a._device, a._index = tensors, device, device.index if device.type == "cuda" else None
     return a
 
 
 def _launch(fn, a, stream):
     """Enqueue on `stream` (None: torch's current stream on the tensors' device), with
-    that device current."""
-    dev = a._device
-    if dev.type != "cuda" or dev.index == torch.cuda.current_device():
-        _ok(fn(ctypes.byref(a), _stream(stream)))
-        return
-    with torch.cuda.device(dev):
-        _ok(fn(ctypes.byref(a), _stream(stream)))
+    that device current.  (The raw queries below: a decode step makes many such calls of
+    a few microseconds each, and torch's stream and device objects cost as much again.)"""
+    i = a._index
+    if i is None or i == torch._C._cuda_getDevice():
+        raw = torch._C._cuda_getCurrentRawStream(i) if stream is None and i is not None else _stream(stream)
+        st = fn(ctypes.byref(a), raw)
+    else:
+        with torch.cuda.device(i):
+            st = fn(ctypes.byref(a), _stream(stream))
+    if st:
+        _ok(st)
 
 
 def paged_cache(K_pages, V_pages, page_table) -> tsa_paged_cache:
