@@ -12,6 +12,13 @@ namespace tsa {
 
 constexpr int kPagedSms = 148;
 
+// 2^x by the special-function unit (about 2^-22 of the value; below 2^-126: 0)
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+    return y;
+}
+
 struct Bf16 {
     static constexpr bool kHalf = false;
     static __device__ __forceinline__ uint32_t pack(float lo, float hi) {

@@ -53,6 +53,7 @@ constexpr int kPxBars = kPxRing + kPxStages * kPxStage;
 constexpr int kPxSmem = kPxBars + 256;
 constexpr int kPxJoinStride = kD + 4;         // floats of a row handed from stream 1 to stream 0
 constexpr int kPxTmemCols = 512;
+constexpr int kPxPolyEvery = 4;               // every 4th pair of weights by polynomial, the others by the special-function unit
 static_assert(kPxTile * kPxJoinStride * 4 <= kPxStages * kPxStage, "the rows handed over fit the ring");
 
 struct PxArgs {
@@ -69,6 +70,14 @@ __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence:
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
 __device__ __forceinline__ void tc_commit(unsigned bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar) : "memory");
+}
+
+// true in one lane of a warp that runs this together: what it issues is then known to be
+// issued once (under a test of the lane number an MMA took 100 cycles to issue instead of 64)
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+    return one != 0;
 }
 
 __device__ __forceinline__ void tm_ld32(uint32_t (&r)[32], uint32_t addr) {
@@ -128,6 +137,53 @@ __device__ constexpr uint32_t px_idesc(bool b_mn) {
            ((uint32_t)(kPxTile >> 4) << 24);
 }
 
+// ---- two fp32 values in one 64-bit register
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;\n" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t dup2(float x) { return pack2(__float_as_uint(x), __float_as_uint(x)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {  // NaN if one is
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// 2^x of two values on the FMA pipe, for x <= 8: x = n + f with n the nearest
+// integer (adding 1.5 * 2^23 rounds to it), 2^f by the polynomial of degree 4 with the
+// smallest largest relative error on [-1/2, 1/2] (2.6e-6, found by the exchange
+// algorithm), n added to the exponent.  Below 2^-125 the result is 2^-125.
+__device__ __forceinline__ void poly_ex2(uint64_t x, float& p0, float& p1) {
+    float a, b;
+    unpack2(x, a, b);
+    x = pack2(__float_as_uint(fmaxf(a, -125.f)), __float_as_uint(fmaxf(b, -125.f)));
+    const uint64_t t = add2(x, dup2(12582912.f));
+    const uint64_t f = add2(x, fma2(add2(t, dup2(-12582912.f)), dup2(-1.f), 0ull));
+    uint64_t p = fma2(f, dup2(0.009570102207362652f), dup2(0.05591785907745361f));
+    p = fma2(f, p, dup2(0.240247443318367f));
+    p = fma2(f, p, dup2(0.6931217908859253f));
+    p = fma2(f, p, dup2(0.9999992847442627f));
+    float t0, t1;
+    unpack2(t, t0, t1);
+    unpack2(p, a, b);
+    p0 = __uint_as_float(__float_as_uint(a) + (__float_as_uint(t0) << 23));
+    p1 = __uint_as_float(__float_as_uint(b) + (__float_as_uint(t1) << 23));
+}
+
 template <class E>
 __global__ void __launch_bounds__(kPxThreads, 1)
 prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const PxArgs a) {
@@ -181,17 +237,20 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             mbar_init_fence();
         }
     } else if (warp < 8) {  // Q: row r of stream s at half * 16 KB + r * 128 B, 16-byte chunks swizzled; rows past R are zeros
-        const int rows = pair ? kPxRows : kPxTile;
-        for (int i = tid; i < rows * 16; i += 256) {
-            const int r = i >> 4, c = i & 15, gr = row0 + r;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (gr < R) {
-                const int b = gr / a.G, j = gr - b * a.G;
-                v = *reinterpret_cast<const uint4*>(a.Q + ((long long)b * a.Hq + h * a.G + j) * kD + c * 8);
-            }
-            const int rr = r & (kPxTile - 1);
-            unsigned char* dst = px_smem + kPxQ + (r >> 7) * kPxStage + (c >> 3) * kPxHalf + rr * 128 + (((c & 7) ^ (rr & 7)) << 4);
-            *reinterpret_cast<uint4*>(dst) = v;
+        // (all of a thread's loads are in flight at once)
+        const int c = tid & 15;
+        uint4 v[kPxRows / 16];
+#pragma unroll
+        for (int i = 0; i < kPxRows / 16; ++i) {
+            const int gr = row0 + i * 16 + (tid >> 4), b = gr / a.G;
+            v[i] = make_uint4(0, 0, 0, 0);
+            if (gr < R) v[i] = *reinterpret_cast<const uint4*>(a.Q + ((long long)b * a.Hq + h * a.G + gr - b * a.G) * kD + c * 8);
+        }
+#pragma unroll
+        for (int i = 0; i < kPxRows / 16; ++i) {
+            const int r = i * 16 + (tid >> 4), rr = r & (kPxTile - 1);
+            *reinterpret_cast<uint4*>(px_smem + kPxQ + (r >> 7) * kPxStage + (c >> 3) * kPxHalf + rr * 128 +
+                                      (((c & 7) ^ (rr & 7)) << 4)) = v[i];
         }
         fence_proxy_async();
     }
@@ -243,16 +302,16 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         for (int p = max(0, pos - kPxStages); p < pos; ++p) mbar_wait(full(p % kPxStages), (p / kPxStages) & 1, nullptr);
         __syncwarp();
       } else if (warp == 8) {
-        // ---- MMA issuer
-        if (lane == 0) {
-            bool ok = true;
-            auto stage = [&](int pos) { return smem0 + kPxRing + pos % kPxStages * kPxStage; };
-            auto loaded = [&](int pos) { return mbar_wait(full(pos % kPxStages), (pos / kPxStages) & 1, a.flag); };
-            auto product_s = [&](int s, int i) {
-                const int pos = 2 * tile_of(s, i);
-                if (!loaded(pos)) return false;
-                tc_fence_after();
-                const uint32_t q = desc_k(smem0 + kPxQ + (pair ? s : 0) * kPxStage), kt = desc_k(stage(pos));
+        // ---- MMA issuer: the warp walks and waits together, one lane issues
+        bool ok = true;
+        auto stage = [&](int pos) { return smem0 + kPxRing + pos % kPxStages * kPxStage; };
+        auto loaded = [&](int pos) { return mbar_wait(full(pos % kPxStages), (pos / kPxStages) & 1, a.flag); };
+        auto product_s = [&](int s, int i) {
+            const int pos = 2 * tile_of(s, i);
+            if (!__all_sync(0xffffffffu, loaded(pos))) return false;
+            tc_fence_after();
+            const uint32_t q = desc_k(smem0 + kPxQ + (pair ? s : 0) * kPxStage), kt = desc_k(stage(pos));
+            if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     const uint32_t off = ((k >> 2) * kPxHalf + (k & 3) * 32) >> 4;
@@ -260,37 +319,41 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                 }
                 tc_commit(sfull(s));
                 if (!pair || s == 1) tc_commit(empty(pos % kPxStages));
-                return true;
-            };
-            auto product_o = [&](int s, int i) {
-                const int pos = 2 * tile_of(s, i) + 1;
-                if (!mbar_wait(pfull(s), i & 1, a.flag) || !loaded(pos)) return false;
-                tc_fence_after();
-                const uint32_t vt = desc_mn(stage(pos));
+            }
+            __syncwarp();
+            return true;
+        };
+        auto product_o = [&](int s, int i) {
+            const int pos = 2 * tile_of(s, i) + 1;
+            if (!__all_sync(0xffffffffu, loaded(pos) && mbar_wait(pfull(s), i & 1, a.flag))) return false;
+            tc_fence_after();
+            const uint32_t vt = desc_mn(stage(pos));
+            if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     tc_mma_ts(tmem + 256 + s * 128, tmem + s * 128 + k * 8, vt + k * (2048 >> 4), px_idesc<E>(true), i + k > 0);
                 if (!pair || s == 1) tc_commit(empty(pos % kPxStages));
                 if (i + 1 == count(s)) tc_commit(ofull(s));
-                return true;
-            };
-            for (int s = 0; s < 2 && ok; ++s)
-                if (count(s) > 0) ok = product_s(s, 0);
-            for (int i = 0; ok && i < count(0); ++i) {
-                for (int s = 0; s < 2 && ok; ++s) {
-                    if (i < count(s)) ok = product_o(s, i);
-                    // (S of the next tile replaces this tile's P: the tensor core takes its instructions in order)
-                    if (ok && i + 1 < count(s)) ok = product_s(s, i + 1);
-                }
             }
-            // the last products have been computed before TMEM is freed: the softmax
-            // warps waited for them, unless a wait gave up
-            if (!ok) {
-                tc_commit(drain);
-                mbar_wait(drain, 0, nullptr);
+            __syncwarp();
+            return true;
+        };
+        for (int s = 0; s < 2 && ok; ++s)
+            if (count(s) > 0) ok = product_s(s, 0);
+        for (int i = 0; ok && i < count(0); ++i) {
+            for (int s = 0; s < 2 && ok; ++s) {
+                if (i < count(s)) ok = product_o(s, i);
+                // (S of the next tile replaces this tile's P: the tensor core takes its instructions in order)
+                if (ok && i + 1 < count(s)) ok = product_s(s, i + 1);
             }
         }
-        __syncwarp();
+        // the last products have been computed before TMEM is freed: the softmax
+        // warps waited for them, unless a wait gave up
+        if (!ok) {
+            if (elect_one()) tc_commit(drain);
+            __syncwarp();
+            mbar_wait(drain, 0, nullptr);
+        }
       }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 224;\n");
@@ -327,16 +390,23 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                         if (col >= nv || !(valid >> (col >> box_log) & 1u)) x[c][j] = 0xff800000u;  // -inf
                     }
             }
-            float mx = -INFINITY;
+            float mq[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < 4; ++c) {
+                mq[c] = max3(__uint_as_float(x[c][0]), __uint_as_float(x[c][1]), __uint_as_float(x[c][2]));
 #pragma unroll
-                for (int j = 0; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(x[c][j]));
-            mx *= a.scale_log2;
+                for (int j = 3; j < 31; j += 2) mq[c] = max3(mq[c], __uint_as_float(x[c][j]), __uint_as_float(x[c][j + 1]));
+            }
+            float mx = max3(mq[0], mq[1], __uint_as_float(x[0][31]));
+            mx = max3(mx, mq[2], __uint_as_float(x[1][31]));
+            mx = max3(mx, mq[3], __uint_as_float(x[2][31]));
+            mx = max3(mx, __uint_as_float(x[3][31]), -INFINITY) * a.scale_log2;
+            // a NaN or an infinite score: the row's result is NaN, as the softmax's is
+            if (!(mx < INFINITY)) l = NAN, mx = m;
             // rescale when some row's maximum has left the range that the sums were formed for
             const bool grow = mx > m + 8.f || (m == -INFINITY && mx > m);
             if (__any_sync(0xffffffffu, grow)) {
-                const float f = grow ? (m == -INFINITY ? 0.f : exp2f(m - mx)) : 1.f;
+                const float f = grow ? (m == -INFINITY ? 0.f : ex2(m - mx)) : 1.f;
                 if (grow) m = mx;
                 l *= f;
                 if (i > 0) {
@@ -351,21 +421,33 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                     }
                 }
             }
-            const float ms = m == -INFINITY ? 0.f : -m;
+            const uint64_t scale2 = dup2(a.scale_log2), shift2 = dup2(m == -INFINITY ? 0.f : -m);
+            uint64_t l0 = 0, l1 = 0;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 uint32_t p[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
-                    const float a0 = __uint_as_float(x[2 * c + (j >> 4)][(2 * j) & 31]);
-                    const float a1 = __uint_as_float(x[2 * c + (j >> 4)][(2 * j + 1) & 31]);
-                    const float p0 = exp2f(fmaf(a0, a.scale_log2, ms)), p1 = exp2f(fmaf(a1, a.scale_log2, ms));
-                    l += p0;
-                    l += p1;
+                    const uint64_t y = fma2(pack2(x[2 * c + (j >> 4)][(2 * j) & 31], x[2 * c + (j >> 4)][(2 * j + 1) & 31]), scale2, shift2);
+                    float p0, p1;
+                    if (j % kPxPolyEvery == kPxPolyEvery - 1) {
+                        poly_ex2(y, p0, p1);
+                    } else {
+                        unpack2(y, p0, p1);
+                        p0 = ex2(p0), p1 = ex2(p1);
+                    }
+                    const uint64_t pp = pack2(__float_as_uint(p0), __float_as_uint(p1));
+                    if (j & 1)
+                        l1 = add2(l1, pp);
+                    else
+                        l0 = add2(l0, pp);
                     p[j] = E::pack(p0, p1);
                 }
                 tm_st32(ts + c * 32, p);
             }
+            float la, lb;
+            unpack2(add2(l0, l1), la, lb);
+            l += la + lb;
             if (nv < kPxTile) {  // zero V's rows past the end (the boxes past it came as zeros)
                 const int pos = 2 * tile_of(s, i) + 1;
                 ok = __all_sync(0xffffffffu, mbar_wait(full(pos % kPxStages), (pos / kPxStages) & 1, a.flag));
@@ -381,6 +463,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             tc_fence_before();
             mbar_arrive(pfull(s));
         }
+        if (m == -INFINITY && l == l) l = 0.f;  // no column of a row of the prefix (each left a 2^-125)
         if (ok && n > 0) ok = __all_sync(0xffffffffu, mbar_wait(ofull(s), 0, a.flag));
         tc_fence_after();
         float* join = reinterpret_cast<float*>(px_smem + kPxRing);
