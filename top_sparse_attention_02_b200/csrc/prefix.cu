@@ -8,20 +8,23 @@
 // K and V, so up to about 250 rows HBM bounds it and above the tensor cores do:
 // both contractions run on tcgen05, tiles of 128 query rows x 128 prefix rows.
 //
-// A CTA (one per SM, 12 warps) takes up to 256 rows of one kv-head over one split
+// A CTA (one per SM, 20 warps) takes up to 256 rows of one kv-head over one split
 // of the prefix, as two streams of 128 rows that take turns on the tensor cores:
-// while one stream's softmax runs on its four warps (a row per thread), the other's
-// products are computed.
-//   warp 9   TMA producer: K and V tiles of 128 prefix rows (boxes of as many rows as
+// while one stream's softmax runs on its eight warps, the other's products are computed.
+//   warp 17  TMA producer: K and V tiles of 128 prefix rows (boxes of as many rows as
 //            a page allows, 128-byte swizzle) into a ring of 5 stages of 32 KB;
-//   warp 8   MMA issuer: S = Q K^T into TMEM (128 columns a stream), then
-//            O += P V with P read from TMEM and V as stored (the MN-major operand);
-//   warps 0-3, 4-7  softmax of stream 0, 1: S from TMEM, the running maximum, P =
-//            2^(S - m) in 16 bits over S's columns; l in fp32.  O is rescaled in
-//            TMEM only when the maximum has grown by more than 2^8 (the result is the
-//            same: all sums are relative to the maximum they were formed with).
-//   warps 10, 11 only make warps 8-11 a warpgroup that hands registers to the softmax
-//            (168 a thread at launch; 56 here and 224 there).
+//   warps 16, 18  MMA issuers of stream 0, 1: S = Q K^T into TMEM (128 columns a
+//            stream), then O += P V with P read from TMEM and V as stored (the MN-major
+//            operand).  (One warp for both streams spent 2000 cycles a turn on its waits
+//            and its issuing, beside 1030 of products: the streams waited for it.)
+//   warps 0-7, 8-15  softmax of stream 0, 1: half a row of S a thread (one thread a
+//            row took 1650 cycles a tile, longer than the other stream's products), the
+//            halves' maxima exchanged through shared memory; P = 2^(S - m) in 16 bits
+//            over S's columns, l in fp32.  O is rescaled in TMEM only when the maximum
+//            has grown by more than 2^8 (the result is the same: all sums are relative
+//            to the maximum they were formed with).
+//   warp 19  only makes warps 16-19 a warpgroup that hands registers to the softmax
+//            (96 a thread at launch; 56 here and 104 there: 4 x 104 + 56 <= 5 x 96).
 // TMEM is full: 2 x (S 128 + O 128) columns.  When 128 rows or fewer are left for a
 // CTA, both streams take the same rows and every other tile, and are joined at the
 // end in shared memory.
@@ -41,7 +44,8 @@
 
 namespace tsa {
 
-constexpr int kPxThreads = 384;
+constexpr int kPxSoftWarps = 16;
+constexpr int kPxThreads = 32 * (kPxSoftWarps + 4);
 constexpr int kPxTile = 128;                  // query rows of a stream, prefix rows of a tile
 constexpr int kPxRows = 2 * kPxTile;          // query rows of a CTA
 constexpr int kPxHalf = kPxTile * 128;        // 64 elements of 128 rows: 16 KB
@@ -50,7 +54,8 @@ constexpr int kPxStages = 5;
 constexpr int kPxQ = 0;                       // Q of both streams, 64 KB
 constexpr int kPxRing = 2 * kPxStage;
 constexpr int kPxBars = kPxRing + kPxStages * kPxStage;
-constexpr int kPxSmem = kPxBars + 256;
+constexpr int kPxMax = kPxBars + 256;            // the halves' maxima: [stream][half][row]
+constexpr int kPxSmem = kPxMax + 2 * 2 * kPxTile * 4;
 constexpr int kPxJoinStride = kD + 4;         // floats of a row handed from stream 1 to stream 0
 constexpr int kPxTmemCols = 512;
 constexpr int kPxPolyEvery = 4;               // every 4th pair of weights by polynomial, the others by the special-function unit
@@ -99,6 +104,14 @@ __device__ __forceinline__ void tm_st32(uint32_t addr, const uint32_t (&r)[32]) 
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
         "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16};\n" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
 __device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
@@ -196,8 +209,9 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     auto sfull = [&](int s) { return bar0 + (2 * kPxStages + s) * 8; };
     auto pfull = [&](int s) { return bar0 + (2 * kPxStages + 2 + s) * 8; };
     auto ofull = [&](int s) { return bar0 + (2 * kPxStages + 4 + s) * 8; };
-    const unsigned drain = bar0 + (2 * kPxStages + 6) * 8;
-    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 2 * kPxStages + 7);
+    auto drain = [&](int s) { return bar0 + (2 * kPxStages + 6 + s) * 8; };
+    auto turn = [&](int s) { return bar0 + (2 * kPxStages + 8 + s) * 8; };
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 2 * kPxStages + 10);
     const int box_log = 4 + a.box_log, box = 1 << box_log, chunks = kPxTile >> box_log;
 
     griddep_wait();
@@ -220,35 +234,69 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     auto count = [&](int s) { return pair ? nt : (nt - s + 1) >> 1; };
     auto tile_of = [&](int s, int i) { return pair ? i : 2 * i + s; };  // (of this CTA's)
 
-    if (warp == 8) {
+    // ---- the producer's loads (warp 17): K of tile t at ring position 2t, V at 2t + 1
+    const unsigned smem0 = su32(px_smem);
+    const uint64_t pol = evict_first_policy();
+    int load_pos = 0, load_row = 0, load_page = 0;  // this lane's box of the tile of load_pos
+    auto load_next = [&] {
+        const int t = load_pos >> 1, kv = load_pos & 1, chunk = lane >> 1, half = lane & 1;
+        const bool mine = chunk < chunks;
+        if (!kv) {
+            const int r = (t0 + t) * kPxTile + chunk * box, pg = r / a.page_size;
+            load_row = r - pg * a.page_size;
+            load_page = a.num_pages;  // outside the map: zeros
+            if (mine && r < a.prefix_len) {
+                load_page = table[pg];
+                if (load_page < 0 || load_page >= a.num_pages) {
+                    atomicOr(a.flag, kFlagBounds);
+                    load_page = a.num_pages;
+                }
+            }
+        }
+        const int st = load_pos % kPxStages;
+        if (lane == 0) mbar_arrive_tx(full(st), kPxStage);
+        __syncwarp();
+        if (mine)
+            tma_4d(smem0 + kPxRing + st * kPxStage + half * kPxHalf + chunk * box * 128, kv ? &vmap : &kmap, half * 64,
+                   load_row, h, load_page, full(st), pol);
+        ++load_pos;
+    };
+
+    if (warp == 16) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(su32(s_tmem)),
                      "r"(kPxTmemCols)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
-    } else if (warp == 9) {
+    } else if (warp == 17) {
         if (lane == 0) {
-            for (int i = 0; i < 2 * kPxStages; ++i) mbar_init(bar0 + i * 8, 1);
+            for (int i = 0; i < kPxStages; ++i) {
+                mbar_init(full(i), 1);
+                mbar_init(empty(i), pair ? 2 : 1);  // the streams that use a tile
+            }
             for (int s = 0; s < 2; ++s) {
                 mbar_init(sfull(s), 1);
-                mbar_init(pfull(s), kPxTile);
+                mbar_init(pfull(s), 2 * kPxTile);
                 mbar_init(ofull(s), 1);
+                mbar_init(drain(s), 1);
+                mbar_init(turn(s), 1);
             }
-            mbar_init(drain, 1);
             mbar_init_fence();
         }
-    } else if (warp < 8) {  // Q: row r of stream s at half * 16 KB + r * 128 B, 16-byte chunks swizzled; rows past R are zeros
+        __syncwarp();
+        while (load_pos < 2 * nt && load_pos < kPxStages) load_next();  // the ring is empty: nothing to wait for
+    } else if (warp < kPxSoftWarps) {  // Q: row r of stream s at half * 16 KB + r * 128 B, 16-byte chunks swizzled; rows past R are zeros
         // (all of a thread's loads are in flight at once)
         const int c = tid & 15;
-        uint4 v[kPxRows / 16];
+        uint4 v[kPxRows / 32];
 #pragma unroll
-        for (int i = 0; i < kPxRows / 16; ++i) {
-            const int gr = row0 + i * 16 + (tid >> 4), b = gr / a.G;
+        for (int i = 0; i < kPxRows / 32; ++i) {
+            const int gr = row0 + i * 32 + (tid >> 4), b = gr / a.G;
             v[i] = make_uint4(0, 0, 0, 0);
             if (gr < R) v[i] = *reinterpret_cast<const uint4*>(a.Q + ((long long)b * a.Hq + h * a.G + gr - b * a.G) * kD + c * 8);
         }
 #pragma unroll
-        for (int i = 0; i < kPxRows / 16; ++i) {
-            const int r = i * 16 + (tid >> 4), rr = r & (kPxTile - 1);
+        for (int i = 0; i < kPxRows / 32; ++i) {
+            const int r = i * 32 + (tid >> 4), rr = r & (kPxTile - 1);
             *reinterpret_cast<uint4*>(px_smem + kPxQ + (r >> 7) * kPxStage + (c >> 3) * kPxHalf + rr * 128 +
                                       (((c & 7) ^ (rr & 7)) << 4)) = v[i];
         }
@@ -259,110 +307,81 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
     // TMEM columns: S of stream s at s * 128 (P over its first 64), O at 256 + s * 128
-    const unsigned smem0 = su32(px_smem);
 
-    if (warp >= 8) {
+    if (warp >= kPxSoftWarps) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 56;\n");
-      if (warp == 9) {
-        // ---- TMA producer: K of tile t at ring position 2t, V at 2t + 1
-        const int chunk = lane >> 1, half = lane & 1;
-        const bool mine = chunk < chunks;
-        const uint64_t pol = evict_first_policy();
-        auto page_of = [&](int t, int* row) {  // this lane's box of tile t0 + t
-            const int r = (t0 + t) * kPxTile + chunk * box, pg = r / a.page_size;
-            *row = r - pg * a.page_size;
-            if (!mine || t >= nt || r >= a.prefix_len) return a.num_pages;  // outside the map: zeros
-            int page = table[pg];
-            if (page < 0 || page >= a.num_pages) {
-                atomicOr(a.flag, kFlagBounds);
-                page = a.num_pages;
-            }
-            return page;
-        };
-        int pos = 0, row, page = page_of(0, &row);
+      if (warp == 17) {
+        // ---- TMA producer
         bool ok = true;
-        for (int t = 0; t < nt && ok; ++t) {
-            int nrow;
-            const int npage = page_of(t + 1, &nrow);
-            for (int kv = 0; kv < 2 && ok; ++kv, ++pos) {
-                const int st = pos % kPxStages, use = pos / kPxStages;
-                if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(empty(st), (use - 1) & 1, a.flag));
-                if (!ok) break;
-                if (lane == 0) mbar_arrive_tx(full(st), kPxStage);
-                __syncwarp();
-                if (mine) {
-                    const unsigned dst = smem0 + kPxRing + st * kPxStage + half * kPxHalf + chunk * box * 128;
-                    tma_4d(dst, kv ? &vmap : &kmap, half * 64, row, h, page, full(st), pol);
-                }
-            }
-            row = nrow;
-            page = npage;
+        while (load_pos < 2 * nt) {
+            ok = __all_sync(0xffffffffu, mbar_wait(empty(load_pos % kPxStages), (load_pos / kPxStages - 1) & 1, a.flag));
+            if (!ok) break;
+            load_next();
         }
         // what was requested has landed before the CTA leaves (at once, unless a wait gave up)
-        for (int p = max(0, pos - kPxStages); p < pos; ++p) mbar_wait(full(p % kPxStages), (p / kPxStages) & 1, nullptr);
+        for (int p = max(0, load_pos - kPxStages); p < load_pos; ++p)
+            mbar_wait(full(p % kPxStages), (p / kPxStages) & 1, nullptr);
         __syncwarp();
-      } else if (warp == 8) {
-        // ---- MMA issuer: the warp walks and waits together, one lane issues
+      } else if (warp != 19) {
+        // ---- MMA issuer of stream s: the warp walks and waits together, one lane issues
+        const int s = (warp - 16) >> 1, n = count(s);
+        const uint32_t ts = tmem + s * 128, to = ts + 256, q = desc_k(smem0 + kPxQ + (pair ? s : 0) * kPxStage);
         bool ok = true;
-        auto stage = [&](int pos) { return smem0 + kPxRing + pos % kPxStages * kPxStage; };
-        auto loaded = [&](int pos) { return mbar_wait(full(pos % kPxStages), (pos / kPxStages) & 1, a.flag); };
-        auto product_s = [&](int s, int i) {
-            const int pos = 2 * tile_of(s, i);
-            if (!__all_sync(0xffffffffu, loaded(pos))) return false;
+        auto loaded = [&](int pos) {
+            return __all_sync(0xffffffffu, mbar_wait(full(pos % kPxStages), (pos / kPxStages) & 1, a.flag));
+        };
+        // Per turn: O += P V of tile i, then S of tile i + 1 over the same columns (the tensor
+        // core takes a warp's instructions in order).  The streams' turns alternate, so
+        // that one's products are computed during the other's softmax: left to
+        // themselves the two fall into step, both softmaxes, then both products.
+        for (int i = -1; i < n && ok; ++i) {
+            const int pv = i >= 0 ? 2 * tile_of(s, i) + 1 : -1, pk = i + 1 < n ? 2 * tile_of(s, i + 1) : -1;
+            const int turns = i + 1 + s;  // of the other stream's that came before
+            if (pv >= 0) ok = loaded(pv);
+            if (pk >= 0) ok = ok && loaded(pk);
+            if (turns > 0) ok = ok && __all_sync(0xffffffffu, mbar_wait(turn(s), (turns - 1) & 1, a.flag));
+            if (pv >= 0) ok = ok && __all_sync(0xffffffffu, mbar_wait(pfull(s), i & 1, a.flag));
+            if (!ok) break;
             tc_fence_after();
-            const uint32_t q = desc_k(smem0 + kPxQ + (pair ? s : 0) * kPxStage), kt = desc_k(stage(pos));
+            const uint32_t vt = desc_mn(smem0 + kPxRing + pv % kPxStages * kPxStage);
+            const uint32_t kt = desc_k(smem0 + kPxRing + pk % kPxStages * kPxStage);
             if (elect_one()) {
+                if (pv >= 0) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const uint32_t off = ((k >> 2) * kPxHalf + (k & 3) * 32) >> 4;
-                    tc_mma_ss(tmem + s * 128, q + off, kt + off, px_idesc<E>(false), k > 0);
+                    for (int k = 0; k < 8; ++k) tc_mma_ts(to, ts + k * 8, vt + k * (2048 >> 4), px_idesc<E>(true), i + k > 0);
+                    tc_commit(empty(pv % kPxStages));
+                    if (i + 1 == n) tc_commit(ofull(s));
                 }
-                tc_commit(sfull(s));
-                if (!pair || s == 1) tc_commit(empty(pos % kPxStages));
-            }
-            __syncwarp();
-            return true;
-        };
-        auto product_o = [&](int s, int i) {
-            const int pos = 2 * tile_of(s, i) + 1;
-            if (!__all_sync(0xffffffffu, loaded(pos) && mbar_wait(pfull(s), i & 1, a.flag))) return false;
-            tc_fence_after();
-            const uint32_t vt = desc_mn(stage(pos));
-            if (elect_one()) {
+                if (pk >= 0) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    tc_mma_ts(tmem + 256 + s * 128, tmem + s * 128 + k * 8, vt + k * (2048 >> 4), px_idesc<E>(true), i + k > 0);
-                if (!pair || s == 1) tc_commit(empty(pos % kPxStages));
-                if (i + 1 == count(s)) tc_commit(ofull(s));
+                    for (int k = 0; k < 8; ++k) {
+                        const uint32_t off = ((k >> 2) * kPxHalf + (k & 3) * 32) >> 4;
+                        tc_mma_ss(ts, q + off, kt + off, px_idesc<E>(false), k > 0);
+                    }
+                    tc_commit(sfull(s));
+                    tc_commit(empty(pk % kPxStages));
+                }
+                mbar_arrive(turn(1 - s));
             }
             __syncwarp();
-            return true;
-        };
-        for (int s = 0; s < 2 && ok; ++s)
-            if (count(s) > 0) ok = product_s(s, 0);
-        for (int i = 0; ok && i < count(0); ++i) {
-            for (int s = 0; s < 2 && ok; ++s) {
-                if (i < count(s)) ok = product_o(s, i);
-                // (S of the next tile replaces this tile's P: the tensor core takes its instructions in order)
-                if (ok && i + 1 < count(s)) ok = product_s(s, i + 1);
-            }
         }
         // the last products have been computed before TMEM is freed: the softmax
         // warps waited for them, unless a wait gave up
         if (!ok) {
-            if (elect_one()) tc_commit(drain);
+            if (elect_one()) tc_commit(drain(s));
             __syncwarp();
-            mbar_wait(drain, 0, nullptr);
+            mbar_wait(drain(s), 0, nullptr);
         }
       }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;\n");
-        // ---- softmax of stream s: this thread's row
-        const int s = warp >> 2, q = warp & 3;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;\n");
+        // ---- softmax of stream s: this thread's half (64 columns) of a row
+        const int s = warp >> 3, hf = warp >> 2 & 1, q = warp & 3, row = q * 32 + lane;
         const int n = count(s);
-        const uint32_t ts = tmem + ((uint32_t)(q * 32) << 16) + s * 128, to = ts + 256;
+        const uint32_t ts = tmem + ((uint32_t)(q * 32) << 16) + s * 128, to = ts + 256 + hf * 64;
+        float* maxima = reinterpret_cast<float*>(px_smem + kPxMax) + s * 2 * kPxTile;
         float m = -INFINITY, l = 0.f;
-        bool ok = true;
+        bool ok = true;  // (after a wait that gave up the barriers below are still kept)
         for (int i = 0; i < n; ++i) {
             const int t = t0 + tile_of(s, i);
             // the tile's columns that are rows of the prefix: a bit per box, and those before the end
@@ -374,33 +393,37 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             }
             const unsigned valid = __ballot_sync(0xffffffffu, good);
             const int nv = min(kPxTile, a.prefix_len - t * kPxTile);
-            ok = __all_sync(0xffffffffu, mbar_wait(sfull(s), i & 1, a.flag));
-            if (!ok) break;
-            tc_fence_after();
-            uint32_t x[4][32];
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(sfull(s), i & 1, a.flag));
+            uint32_t x[2][32];
+            if (ok) {
+                tc_fence_after();
+                tm_ld32(x[0], ts + hf * 64);
+                tm_ld32(x[1], ts + hf * 64 + 32);
+                tm_wait_ld();
+                if (valid != (0xffffffffu >> (32 - chunks)) || nv < kPxTile) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tm_ld32(x[c], ts + c * 32);
-            tm_wait_ld();
-            if (valid != (0xffffffffu >> (32 - chunks)) || nv < kPxTile) {
+                    for (int c = 0; c < 2; ++c)
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                        for (int j = 0; j < 32; ++j) {
+                            const int col = hf * 64 + c * 32 + j;
+                            if (col >= nv || !(valid >> (col >> box_log) & 1u)) x[c][j] = 0xff800000u;  // -inf
+                        }
+                }
+                float mq[4];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const int col = c * 32 + j;
-                        if (col >= nv || !(valid >> (col >> box_log) & 1u)) x[c][j] = 0xff800000u;  // -inf
-                    }
+                for (int c = 0; c < 4; ++c) {
+                    const uint32_t* y = &x[c >> 1][(c & 1) * 16];
+                    mq[c] = max3(__uint_as_float(y[0]), __uint_as_float(y[1]), __uint_as_float(y[2]));
+#pragma unroll
+                    for (int j = 3; j < 15; j += 2) mq[c] = max3(mq[c], __uint_as_float(y[j]), __uint_as_float(y[j + 1]));
+                    mq[c] = max3(mq[c], __uint_as_float(y[15]), -INFINITY);
+                }
+                maxima[hf * kPxTile + row] = max3(max3(mq[0], mq[1], mq[2]), mq[3], -INFINITY);
             }
-            float mq[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                mq[c] = max3(__uint_as_float(x[c][0]), __uint_as_float(x[c][1]), __uint_as_float(x[c][2]));
-#pragma unroll
-                for (int j = 3; j < 31; j += 2) mq[c] = max3(mq[c], __uint_as_float(x[c][j]), __uint_as_float(x[c][j + 1]));
-            }
-            float mx = max3(mq[0], mq[1], __uint_as_float(x[0][31]));
-            mx = max3(mx, mq[2], __uint_as_float(x[1][31]));
-            mx = max3(mx, mq[3], __uint_as_float(x[2][31]));
-            mx = max3(mx, __uint_as_float(x[3][31]), -INFINITY) * a.scale_log2;
+            // both halves have their S in registers (P goes over it) and each other's maximum
+            asm volatile("bar.sync %0, 256;\n" ::"r"(2 + s) : "memory");
+            if (!ok) continue;
+            float mx = max3(maxima[row], maxima[kPxTile + row], -INFINITY) * a.scale_log2;
             // a NaN or an infinite score: the row's result is NaN, as the softmax's is
             if (!(mx < INFINITY)) l = NAN, mx = m;
             // rescale when some row's maximum has left the range that the sums were formed for
@@ -410,8 +433,8 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                 if (grow) m = mx;
                 l *= f;
                 if (i > 0) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
+#pragma unroll 1
+                    for (int c = 0; c < 2; ++c) {
                         uint32_t o[32];
                         tm_ld32(o, to + c * 32);
                         tm_wait_ld();
@@ -421,14 +444,25 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                     }
                 }
             }
+            if (nv < kPxTile) {  // zero V's rows past the end (the boxes past it came as zeros)
+                const int pos = 2 * tile_of(s, i) + 1;
+                ok = __all_sync(0xffffffffu, mbar_wait(full(pos % kPxStages), (pos / kPxStages) & 1, a.flag));
+                if (!ok) continue;
+                unsigned char* v = px_smem + kPxRing + pos % kPxStages * kPxStage;
+                const int end = min(kPxTile, (nv + box - 1) & -box);
+                for (int j = tid & 255; j < (end - nv) * 16; j += 256)
+                    *reinterpret_cast<uint4*>(v + (j >> 3 & 1) * kPxHalf + (nv + (j >> 4)) * 128 + (j & 7) * 16) =
+                        make_uint4(0, 0, 0, 0);
+                fence_proxy_async();
+            }
             const uint64_t scale2 = dup2(a.scale_log2), shift2 = dup2(m == -INFINITY ? 0.f : -m);
             uint64_t l0 = 0, l1 = 0;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                uint32_t p[32];
+                uint32_t p[16];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const uint64_t y = fma2(pack2(x[2 * c + (j >> 4)][(2 * j) & 31], x[2 * c + (j >> 4)][(2 * j + 1) & 31]), scale2, shift2);
+                for (int j = 0; j < 16; ++j) {
+                    const uint64_t y = fma2(pack2(x[c][2 * j], x[c][2 * j + 1]), scale2, shift2);
                     float p0, p1;
                     if (j % kPxPolyEvery == kPxPolyEvery - 1) {
                         poly_ex2(y, p0, p1);
@@ -443,36 +477,29 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                         l0 = add2(l0, pp);
                     p[j] = E::pack(p0, p1);
                 }
-                tm_st32(ts + c * 32, p);
-            }
-            float la, lb;
-            unpack2(add2(l0, l1), la, lb);
-            l += la + lb;
-            if (nv < kPxTile) {  // zero V's rows past the end (the boxes past it came as zeros)
-                const int pos = 2 * tile_of(s, i) + 1;
-                ok = __all_sync(0xffffffffu, mbar_wait(full(pos % kPxStages), (pos / kPxStages) & 1, a.flag));
-                if (!ok) break;
-                unsigned char* v = px_smem + kPxRing + pos % kPxStages * kPxStage;
-                const int end = min(kPxTile, (nv + box - 1) & -box);
-                for (int j = tid & 127; j < (end - nv) * 16; j += 128)
-                    *reinterpret_cast<uint4*>(v + (j >> 3 & 1) * kPxHalf + (nv + (j >> 4)) * 128 + (j & 7) * 16) =
-                        make_uint4(0, 0, 0, 0);
-                fence_proxy_async();
+                tm_st16(ts + hf * 32 + c * 16, p);
             }
             tm_wait_st();
             tc_fence_before();
             mbar_arrive(pfull(s));
+            float la, lb;
+            unpack2(add2(l0, l1), la, lb);
+            l += la + lb;
         }
         if (m == -INFINITY && l == l) l = 0.f;  // no column of a row of the prefix (each left a 2^-125)
         if (ok && n > 0) ok = __all_sync(0xffffffffu, mbar_wait(ofull(s), 0, a.flag));
         tc_fence_after();
+        // the row's weight is the sum of its halves'
+        asm volatile("bar.sync %0, 256;\n" ::"r"(2 + s) : "memory");
+        maxima[hf * kPxTile + row] = l;
+        asm volatile("bar.sync %0, 256;\n" ::"r"(2 + s) : "memory");
+        l = maxima[row] + maxima[kPxTile + row];
         float* join = reinterpret_cast<float*>(px_smem + kPxRing);
-        const int row = tid & 127;
         if (!pair) {  // stream 1 hands its rows to stream 0
-            asm volatile("bar.sync 1, 256;\n" ::: "memory");  // no product reads the ring any more
+            asm volatile("bar.sync 1, 512;\n" ::: "memory");  // no product reads the ring any more
             if (s == 1 && ok) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
+#pragma unroll 1
+                for (int c = 0; c < 2; ++c) {
                     uint32_t o[32];
                     if (n > 0) {
                         tm_ld32(o, to + c * 32);
@@ -480,13 +507,15 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                     }
 #pragma unroll
                     for (int j = 0; j < 32; j += 4)
-                        *reinterpret_cast<uint4*>(join + row * kPxJoinStride + c * 32 + j) =
+                        *reinterpret_cast<uint4*>(join + row * kPxJoinStride + hf * 64 + c * 32 + j) =
                             n > 0 ? make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]) : make_uint4(0, 0, 0, 0);
                 }
-                join[row * kPxJoinStride + kD] = m;
-                join[row * kPxJoinStride + kD + 1] = l;
+                if (hf == 0) {
+                    join[row * kPxJoinStride + kD] = m;
+                    join[row * kPxJoinStride + kD + 1] = l;
+                }
             }
-            asm volatile("bar.sync 1, 256;\n" ::: "memory");
+            asm volatile("bar.sync 1, 512;\n" ::: "memory");
         }
         const int gr = row0 + (pair ? s * kPxTile : 0) + row;
         if (ok && (pair || s == 0)) {
@@ -496,13 +525,13 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             const float* other = join + row * kPxJoinStride;
             if (!pair) {
                 const float m1 = other[kD], l1 = other[kD + 1], M = fmaxf(m, m1);
-                f0 = m == -INFINITY ? 0.f : exp2f(m - M);
-                f1 = m1 == -INFINITY ? 0.f : exp2f(m1 - M);
+                f0 = m == -INFINITY ? 0.f : ex2(m - M);
+                f1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
                 l = (m == -INFINITY ? l : f0 * l) + (m1 == -INFINITY ? l1 : f1 * l1);
                 m = M;
             }
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) {
                 uint32_t o[32];
                 tm_ld32(o, to + c * 32);
                 tm_wait_ld();
@@ -512,15 +541,15 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                         float4 v = make_float4(__uint_as_float(o[k]), __uint_as_float(o[k + 1]), __uint_as_float(o[k + 2]),
                                                __uint_as_float(o[k + 3]));
                         if (!pair) {
-                            const float4 w = *reinterpret_cast<const float4*>(other + c * 32 + k);
+                            const float4 w = *reinterpret_cast<const float4*>(other + hf * 64 + c * 32 + k);
                             v.x = f0 * v.x + f1 * w.x, v.y = f0 * v.y + f1 * w.y;
                             v.z = f0 * v.z + f1 * w.z, v.w = f0 * v.w + f1 * w.w;
                         }
-                        *reinterpret_cast<float4*>(out + c * 32 + k) = v;
+                        *reinterpret_cast<float4*>(out + hf * 64 + c * 32 + k) = v;
                     }
                 }
             }
-            if (gr < R) {
+            if (gr < R && hf == 0) {
                 out[kD] = m;
                 out[kD + 1] = l;
             }
@@ -528,7 +557,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == 16) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(kPxTmemCols) : "memory");
     }
