@@ -58,7 +58,6 @@ constexpr int kPxMax = kPxBars + 256;            // the halves' maxima: [stream]
 constexpr int kPxSmem = kPxMax + 2 * 2 * kPxTile * 4;
 constexpr int kPxJoinStride = kD + 4;         // floats of a row handed from stream 1 to stream 0
 constexpr int kPxTmemCols = 512;
-constexpr int kPxPolyEvery = 4;               // every 4th pair of weights by polynomial, the others by the special-function unit
 static_assert(kPxTile * kPxJoinStride * 4 <= kPxStages * kPxStage, "the rows handed over fit the ring");
 
 struct PxArgs {
@@ -150,51 +149,10 @@ __device__ constexpr uint32_t px_idesc(bool b_mn) {
            ((uint32_t)(kPxTile >> 4) << 24);
 }
 
-// ---- two fp32 values in one 64-bit register
-__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "r"(lo), "r"(hi));
-    return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
-    asm("mov.b64 {%0, %1}, %2;\n" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t dup2(float x) { return pack2(__float_as_uint(x), __float_as_uint(x)); }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {  // NaN if one is
     float d;
     asm("max.NaN.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
-}
-
-// 2^x of two values on the FMA pipe, for x <= 8: x = n + f with n the nearest
-// integer (adding 1.5 * 2^23 rounds to it), 2^f by the polynomial of degree 4 with the
-// smallest largest relative error on [-1/2, 1/2] (2.6e-6, found by the exchange
-// algorithm), n added to the exponent.  Below 2^-125 the result is 2^-125.
-__device__ __forceinline__ void poly_ex2(uint64_t x, float& p0, float& p1) {
-    float a, b;
-    unpack2(x, a, b);
-    x = pack2(__float_as_uint(fmaxf(a, -125.f)), __float_as_uint(fmaxf(b, -125.f)));
-    const uint64_t t = add2(x, dup2(12582912.f));
-    const uint64_t f = add2(x, fma2(add2(t, dup2(-12582912.f)), dup2(-1.f), 0ull));
-    uint64_t p = fma2(f, dup2(0.009570102207362652f), dup2(0.05591785907745361f));
-    p = fma2(f, p, dup2(0.240247443318367f));
-    p = fma2(f, p, dup2(0.6931217908859253f));
-    p = fma2(f, p, dup2(0.9999992847442627f));
-    float t0, t1;
-    unpack2(t, t0, t1);
-    unpack2(p, a, b);
-    p0 = __uint_as_float(__float_as_uint(a) + (__float_as_uint(t0) << 23));
-    p1 = __uint_as_float(__float_as_uint(b) + (__float_as_uint(t1) << 23));
 }
 
 template <class E>
@@ -455,26 +413,18 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                         make_uint4(0, 0, 0, 0);
                 fence_proxy_async();
             }
-            const uint64_t scale2 = dup2(a.scale_log2), shift2 = dup2(m == -INFINITY ? 0.f : -m);
-            uint64_t l0 = 0, l1 = 0;
+            const float shift = m == -INFINITY ? 0.f : -m;
+            float ls[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 uint32_t p[16];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
-                    const uint64_t y = fma2(pack2(x[c][2 * j], x[c][2 * j + 1]), scale2, shift2);
-                    float p0, p1;
-                    if (j % kPxPolyEvery == kPxPolyEvery - 1) {
-                        poly_ex2(y, p0, p1);
-                    } else {
-                        unpack2(y, p0, p1);
-                        p0 = ex2(p0), p1 = ex2(p1);
-                    }
-                    const uint64_t pp = pack2(__float_as_uint(p0), __float_as_uint(p1));
-                    if (j & 1)
-                        l1 = add2(l1, pp);
-                    else
-                        l0 = add2(l0, pp);
+                    // (a quarter of these by polynomial on the FMA pipe, packed or not, took as long)
+                    const float p0 = ex2(fmaf(__uint_as_float(x[c][2 * j]), a.scale_log2, shift));
+                    const float p1 = ex2(fmaf(__uint_as_float(x[c][2 * j + 1]), a.scale_log2, shift));
+                    ls[2 * j & 3] += p0;
+                    ls[(2 * j & 3) + 1] += p1;
                     p[j] = E::pack(p0, p1);
                 }
                 tm_st16(ts + hf * 32 + c * 16, p);
@@ -482,11 +432,8 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             tm_wait_st();
             tc_fence_before();
             mbar_arrive(pfull(s));
-            float la, lb;
-            unpack2(add2(l0, l1), la, lb);
-            l += la + lb;
+            l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
         }
-        if (m == -INFINITY && l == l) l = 0.f;  // no column of a row of the prefix (each left a 2^-125)
         if (ok && n > 0) ok = __all_sync(0xffffffffu, mbar_wait(ofull(s), 0, a.flag));
         tc_fence_after();
         // the row's weight is the sum of its halves'
