@@ -48,6 +48,8 @@ constexpr int kPgGranule = kPgWarps * kPageRows;   // rows
 constexpr int kPgHalf = kPageRows * 128;           // 64 elements of 16 rows: 2 KB
 constexpr int kPgStage = 4 * kPgHalf;              // K halves, V halves: 8 KB
 constexpr int kPgCtasPerSm = 2;
+constexpr int kPgPieces = 16;  // pieces of a unit that one round of loads joins
+constexpr int kPgLong = 8;     // granules a CTA above which more pieces pay
 constexpr float kNegInf = -INFINITY;
 
 template <int NT>
@@ -111,19 +113,9 @@ __device__ __forceinline__ Span span_of(const PgArgs& a, int b, bool report) {
     return s;
 }
 
-// A row's result out of its sums acc (4 of 128 a lane), maximum M and weight L: into O
-// and lse, or (over a shared prefix) as one more partial of the row.
+// A row's result out of its sums acc (4 of 128 a lane), maximum M and weight L.
 template <class E>
-__device__ __forceinline__ void put_row(const PgArgs& a, long long row, float4 acc, float M, float L, int lane) {
-    if (a.own) {
-        float* p = a.own + row * kPartFloats;
-        __stcg(reinterpret_cast<float4*>(p) + lane, acc);
-        if (lane == 0) {
-            __stcg(p + kD, M);
-            __stcg(p + kD + 1, L);
-        }
-        return;
-    }
+__device__ __forceinline__ void finish_row(const PgArgs& a, long long row, float4 acc, float M, float L, int lane) {
     const float inv = L == 0.f ? 0.f : 1.0f / L;
     uint2 o;
     o.x = E::pack(acc.x * inv, acc.y * inv);
@@ -132,43 +124,76 @@ __device__ __forceinline__ void put_row(const PgArgs& a, long long row, float4 a
     if (a.lse && lane == 0) a.lse[row] = L == 0.f ? kNegInf : M + log2f(L);
 }
 
-// Join n partials of one row, part(i) for i < n, each kPartFloats with M and L after
-// its 128 sums: this lane's 4 sums relative to *M, and the weight *L.  All lanes of
-// the warp; wts holds n floats.
+// The same, or (over a shared prefix) one more partial of the row.
+template <class E>
+__device__ __forceinline__ void put_row(const PgArgs& a, long long row, float4 acc, float M, float L, int lane) {
+    if (!a.own) {
+        finish_row<E>(a, row, acc, M, L, lane);
+        return;
+    }
+    float* p = a.own + row * kPartFloats;
+    __stcg(reinterpret_cast<float4*>(p) + lane, acc);
+    if (lane == 0) __stcg(reinterpret_cast<float2*>(p + kD), make_float2(M, L));
+}
+
+// The weights of n partials of one row, part(i) for i < n, each kPartFloats with its
+// maximum and weight after the 128 sums: wts[i] = 2^(M_i - M), the joint maximum *M
+// and weight *L.  All lanes of the warp.
 template <class Part>
-__device__ __forceinline__ float4 join_row(int n, Part part, float* wts, int lane, float* M_out, float* L_out) {
-    float M = kNegInf;
-    for (int i = lane; i < n; i += 32) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(part(i) + kD));
+__device__ __forceinline__ void join_weights(int n, Part part, float* wts, int lane, float* M_out, float* L_out) {
+    auto ml_of = [&](int i) { return __ldcg(reinterpret_cast<const float2*>(part(i) + kD)); };
+    float2 ml0 = make_float2(kNegInf, 0.f), ml1 = ml0;  // the first 64 stay in registers
+    if (lane < n) ml0 = ml_of(lane);
+    if (lane + 32 < n) ml1 = ml_of(lane + 32);
+    float M = fmaxf(ml0.y > 0.f ? ml0.x : kNegInf, ml1.y > 0.f ? ml1.x : kNegInf);
+    for (int i = lane + 64; i < n; i += 32) {
+        const float2 ml = ml_of(i);
         if (ml.y > 0.f) M = fmaxf(M, ml.x);
     }
 #pragma unroll
     for (int m = 16; m; m >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
     float L = 0.f;
     bool bad = false;  // a NaN weight: the result is NaN, as the softmax's is
-    for (int i = lane; i < n; i += 32) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(part(i) + kD));
+    auto take = [&](int i, float2 ml) {
         const float w = ml.y > 0.f ? exp2f(ml.x - M) : 0.f;
         bad |= ml.y != ml.y;
         wts[i] = w;
         L += w * ml.y;
-    }
+    };
+    if (lane < n) take(lane, ml0);
+    if (lane + 32 < n) take(lane + 32, ml1);
+    for (int i = lane + 64; i < n; i += 32) take(i, ml_of(i));
 #pragma unroll
     for (int m = 16; m; m >>= 1) L += __shfl_xor_sync(0xffffffffu, L, m);
     if (__any_sync(0xffffffffu, bad)) L = NAN;
     __syncwarp();
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int i = 0; i < n; ++i) {
-        const float w = wts[i];
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(part(i)) + lane);
-        if (w == 0.f) continue;  // (a part without a row may hold anything)
-        acc.x = fmaf(w, v.x, acc.x), acc.y = fmaf(w, v.y, acc.y);
-        acc.z = fmaf(w, v.z, acc.z), acc.w = fmaf(w, v.w, acc.w);
-    }
-    __syncwarp();
     *M_out = M;
     *L_out = L;
+}
+
+// This lane's 4 of the 128 sums over the partials i0, i0 + step, ... < n, with the
+// weights that join_weights leaves in wts.  kJoinFlight loads are on their way at a
+// time, the first of them before the weights are known (they come out of L2, at
+// about a microsecond a round).
+constexpr int kJoinFlight = 16;
+template <class Part, class Weights>
+__device__ __forceinline__ float4 join_sums(int n, int i0, int step, Part part, const float* wts, int lane, Weights weights) {
+    float4 v[kJoinFlight], acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    bool first = true;
+    for (int i = i0; i < n || first; i += kJoinFlight * step) {
+#pragma unroll
+        for (int k = 0; k < kJoinFlight; ++k)
+            if (i + k * step < n) v[k] = __ldcg(reinterpret_cast<const float4*>(part(i + k * step)) + lane);
+        if (first) weights();
+        first = false;
+#pragma unroll
+        for (int k = 0; k < kJoinFlight; ++k) {
+            const float w = i + k * step < n ? wts[i + k * step] : 0.f;
+            if (w == 0.f) continue;  // (a part without a row may hold anything)
+            acc.x = fmaf(w, v[k].x, acc.x), acc.y = fmaf(w, v[k].y, acc.y);
+            acc.z = fmaf(w, v[k].z, acc.z), acc.w = fmaf(w, v[k].w, acc.w);
+        }
+    }
     return acc;
 }
 
@@ -239,21 +264,25 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         *before = pre + inc - v;
         return tot;
     };
-    long long total = 0, before;
+    long long total = 0, before, mine = 0;  // (up to kPgThreads sequences: one scan serves for both)
     for (int b0 = 0; b0 < B; b0 += kPgThreads) {
         const int b = b0 + tid;
-        const long long v = b < B ? (long long)span_of<GATHER>(a, b, cta == 0).granules() * Hkv : 0;
-        total += block_sum(v, &before);
+        mine = b < B ? (long long)span_of<GATHER>(a, b, cta == 0).granules() * Hkv : 0;
+        total += block_sum(mine, &before);
     }
-    const long long nc = min((long long)gridDim.x, total);  // CTAs with work: a granule each at least
+    // CTAs with work.  Few units are not spread over more CTAs than it takes to read
+    // them: joining a unit's pieces costs a round trip for each 16 of them.
+    const long long nc = min(min((long long)gridDim.x, total), max((long long)B * Hkv * kPgPieces, total / kPgLong));
     const long long g0 = cta < nc ? total * cta / nc : 0, g1 = cta < nc ? total * (cta + 1) / nc : 0;
-    if (tid == 0) s_b = -1;
     long long run = 0;
     for (int b0 = 0; b0 < B && g0 < g1; b0 += kPgThreads) {  // which sequence holds granule g0
         const int b = b0 + tid;
-        const long long v = b < B ? (long long)span_of<GATHER>(a, b, false).granules() * Hkv : 0;
-        const long long t = block_sum(v, &before);
-        if (v > 0 && run + before <= g0 && g0 < run + before + v) {
+        long long t = total;
+        if (B > kPgThreads) {
+            mine = b < B ? (long long)span_of<GATHER>(a, b, false).granules() * Hkv : 0;
+            t = block_sum(mine, &before);
+        }
+        if (mine > 0 && run + before <= g0 && g0 < run + before + mine) {
             s_b = b;
             s_base = run + before;
         }
@@ -541,7 +570,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             const bool whole = seg0 == cur.s.first() && cur.x + 1 == cur.hi;
             const long long gend = g0 + i + 1, u1 = gend + (cur.hi - cur.x - 1), u0 = u1 - cur.s.granules();
             const long long c0 = ((u0 + 1) * nc - 1) / total, c1 = (u1 * nc - 1) / total;  // its CTAs
-            float* mine = a.pieces + (2LL * cta + (u0 > g0 ? 1 : 0)) * a.G * kPartFloats;
+            float* piece = a.pieces + (2LL * cta + (u0 > g0 ? 1 : 0)) * a.G * kPartFloats;
             for (int g = warp; g < a.G; g += kPgWarps) {
                 float M = kNegInf, L = 0.f, f[kPgWarps];
                 const float* w = merge + g * kPartFloats;
@@ -564,12 +593,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                 if (whole) {
                     put_row<E>(a, (long long)cur.b * a.Hq + cur.h * a.G + g, o, M, L, lane);
                 } else {
-                    float* p = mine + g * kPartFloats;
+                    float* p = piece + g * kPartFloats;
                     __stcg(reinterpret_cast<float4*>(p) + lane, o);
-                    if (lane == 0) {
-                        __stcg(p + kD, M);
-                        __stcg(p + kD + 1, L);
-                    }
+                    if (lane == 0) __stcg(reinterpret_cast<float2*>(p + kD), make_float2(M, L));
                 }
             }
             if (!whole) {
@@ -593,7 +619,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                             return a.pieces + ((2 * c + (second ? 1 : 0)) * a.G + g) * kPartFloats;
                         };
                         float M, L;
-                        const float4 o = join_row(n, part, merge + g * n, lane, &M, &L);
+                        float* wts = merge + g * n;
+                        const float4 o = join_sums(n, 0, 1, part, wts, lane,
+                                                   [&] { join_weights(n, part, wts, lane, &M, &L); });
                         put_row<E>(a, (long long)cur.b * a.Hq + cur.h * a.G + g, o, M, L, lane);
                     }
                 }
@@ -617,43 +645,59 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 }
 
 // Over a shared prefix: every row's partials (the prefix's splits, where the
-// sequence holds the prefix whole, and its own rows' one) into O and lse.  A warp a
-// row: the partials come out of L2.
-constexpr int kJoinThreads = 128;
-constexpr int kMaxParts = 2 * kPagedSms + 1;
-template <class E>
-__global__ void __launch_bounds__(kJoinThreads)
-prefix_join_kernel(const PgArgs a) {
-    __shared__ float wts[kJoinThreads / 32][kMaxParts];
+// sequence holds the prefix whole, and its own rows' one) into O and lse.  W warps
+// a row, each with a part of the partials, whose loads are all on their way at once.
+constexpr int kJoinWarps = 4;
+template <class E, int W>
+__global__ void __launch_bounds__(32 * kJoinWarps)
+prefix_join_kernel(const PgArgs a, int rows) {
+    __shared__ float wts[kJoinWarps][kMaxPrefixSplits + 1];
+    __shared__ float4 sums[kJoinWarps][32];
     griddep_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long row = (long long)blockIdx.x * (kJoinThreads / 32) + warp, rows = (long long)a.c.B * a.Hq;
-    if (row < rows) {
-        const int b = (int)(row / a.Hq);
-        const int n0 = a.lens[b] >= a.pre.prefix_len ? a.pre.splits : 0;
-        auto part = [&](int i) { return i < n0 ? a.pre.parts + (i * rows + row) * kPartFloats : a.own + row * kPartFloats; };
-        float M, L;
-        const float4 o = join_row(n0 + 1, part, wts[warp], lane, &M, &L);
-        PgArgs out = a;
-        out.own = nullptr;
-        put_row<E>(out, row, o, M, L, lane);
-    }
     griddep_launch();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = warp % W;
+    const long long row = (long long)blockIdx.x * (kJoinWarps / W) + warp / W;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float M = kNegInf, L = 0.f;
+    if (row < rows) {
+        const int n0 = a.lens[row / a.Hq] >= a.pre.prefix_len ? a.pre.splits : 0, n = n0 + 1;
+        auto part = [&](int i) {
+            return i < n0 ? a.pre.parts + ((long long)i * rows + row) * kPartFloats : a.own + row * kPartFloats;
+        };
+        o = join_sums(n, w, W, part, wts[warp], lane, [&] { join_weights(n, part, wts[warp], lane, &M, &L); });
+    }
+    if constexpr (W > 1) {
+        sums[warp][lane] = o;
+        __syncthreads();
+#pragma unroll
+        for (int i = 1; i < W; ++i) {
+            const float4 v = sums[warp + i < kJoinWarps ? warp + i : warp][lane];
+            o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+        }
+    }
+    if (row < rows && w == 0) finish_row<E>(a, row, o, M, L, lane);
 }
 
-template <class E>
+template <class E, int W>
 static cudaError_t join_launch(const PgArgs& a, cudaStream_t st) {
-    const long long rows = (long long)a.c.B * a.Hq, per = kJoinThreads / 32;
+    const long long rows = (long long)a.c.B * a.Hq, per = kJoinWarps / W;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((rows + per - 1) / per));
-    cfg.blockDim = dim3(kJoinThreads);
+    cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.stream = st;
     cudaLaunchAttribute attr[1] = {pdl_attr()};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, prefix_join_kernel<E>, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, prefix_join_kernel<E, W>, a, (int)rows);
     note_launch();
     return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// Few rows: four warps each (256 rows of 17 partials 3.6 us, against 7.5 with one);
+// many: one each, which fills the SMs (4096 rows of 10: 7.1 us, against 17 with four).
+template <class E>
+static cudaError_t join_pick(const PgArgs& a, cudaStream_t st) {
+    return (long long)a.c.B * a.Hq <= 8 * kPagedSms ? join_launch<E, kJoinWarps>(a, st) : join_launch<E, 1>(a, st);
 }
 
 template <class E, int NT, bool GATHER>
@@ -710,7 +754,7 @@ cudaError_t launch_paged_attn(const Pages& c, const void* Q, int Hq, const int32
     const int grid = paged_ctas();
     const cudaError_t e = c.half ? paged_pick<F16>(grid, km, vm, a, st) : paged_pick<Bf16>(grid, km, vm, a, st);
     if (e != cudaSuccess || pre.splits == 0) return e;
-    return c.half ? join_launch<F16>(a, st) : join_launch<Bf16>(a, st);
+    return c.half ? join_pick<F16>(a, st) : join_pick<Bf16>(a, st);
 }
 
 }  // namespace tsa

@@ -11,6 +11,7 @@ namespace tsa {
 
 constexpr int kMaxGroup = 16;     // query heads per kv-head that the paged attention takes
 constexpr int kPageRows = 16;     // a page holds a multiple of this many rows
+constexpr int kMaxPrefixSplits = 128;  // partials of a shared prefix's pass a row
 constexpr int kPartFloats = 132;  // a partial of one head: acc[128], M, L, 2 pad (528 B)
 
 // A cache in pages: row j of (sequence b, kv-head h) lies in page

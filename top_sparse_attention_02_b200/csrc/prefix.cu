@@ -515,7 +515,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 static int px_groups(int R) { return (R + kPxRows - 1) / kPxRows; }
 int prefix_max_splits(int Hkv, int R, int prefix_len) {
     const long long items = (long long)Hkv * px_groups(R), nt = ((long long)prefix_len + kPxTile - 1) / kPxTile;
-    return (int)std::min(nt, std::max(1LL, 2 * kPagedSms / std::max(1LL, items)));
+    return (int)std::min({nt, (long long)kMaxPrefixSplits, std::max(1LL, 2 * kPagedSms / std::max(1LL, items))});
 }
 static int px_splits(int Hkv, int R, int prefix_len) {
     const long long items = (long long)Hkv * px_groups(R), nt = ((long long)prefix_len + kPxTile - 1) / kPxTile;
