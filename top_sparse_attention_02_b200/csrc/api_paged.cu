@@ -148,17 +148,17 @@ tsa_status check_ws(const void* ws, size_t ws_bytes, size_t need) {
     return TSA_OK;
 }
 
-// [flag 256 B][a counter per unit, zero between calls][the CTAs' pieces][a shared prefix's partials, and
+// [flag 256 B][each unit's pieces][the CTAs' pieces][a shared prefix's partials, and
 // those of the sequences' own rows]
 struct Layout {
-    size_t counters, pieces, parts, total;
+    size_t units, pieces, parts, total;
 };
 
 Layout layout(const tsa::Pages& c, int Hq, int prefix_len) {
     Layout L;
     size_t off = kFlagBytes;
-    L.counters = off;
-    off += a256((size_t)c.B * c.Hkv * sizeof(unsigned));
+    L.units = off;
+    off += a256((size_t)c.B * c.Hkv * 2 * sizeof(int32_t));
     L.pieces = off;
     off += a256((size_t)2 * tsa::paged_ctas() * (Hq / c.Hkv) * tsa::kPartFloats * sizeof(float));
     L.parts = off;
@@ -189,6 +189,8 @@ tsa_status attn(const tsa_paged_attn_args* a, bool prefix, const char* what, voi
         if (!aligned16(a->Q) || !aligned16(a->O)) return fail(TSA_ERR_INVALID_ARG, "%s: Q and O must be 16-byte aligned", what);
         if (a->O == a->Q) return fail(TSA_ERR_INVALID_ARG, "%s: O must not be Q", what);
     }
+    if ((long long)c.B * c.Hkv * ((c.rows_cap() + 63LL) / 64) > INT32_MAX)
+        return fail(TSA_ERR_UNSUPPORTED, "%s: B*Hkv*max_pages*page_size above 2^37 rows", what);
     const Layout L = layout(c, a->Hq, a->prefix_len);
     TSA_TRY(check_ws(a->ws, a->ws_bytes, L.total));
     if (a->prefix_len > 1 << 30) return fail(TSA_ERR_UNSUPPORTED, "%s: prefix_len=%d above 2^30", what, a->prefix_len);
@@ -203,7 +205,7 @@ tsa_status attn(const tsa_paged_attn_args* a, bool prefix, const char* what, voi
     }
     const cudaError_t e = tsa::launch_paged_attn(c, a->Q, a->Hq, a->seq_lens, a->idx, a->k_per_seq, a->k_max, a->scale,
                                                  a->O, a->lse, reinterpret_cast<float*>(w + L.pieces),
-                                                 reinterpret_cast<unsigned*>(w + L.counters), pre, flag, st);
+                                                 reinterpret_cast<int32_t*>(w + L.units), pre, flag, st);
     if (e != cudaSuccess) return cuda_fail(e, what);
     return TSA_OK;
 }

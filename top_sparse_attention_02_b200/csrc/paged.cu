@@ -13,10 +13,12 @@
 //  - Even work whatever the lengths: the granules (64 rows) of all units are
 //    laid end to end and each CTA takes the same number of them, so a CTA may end
 //    in the middle of one unit and begin in the middle of another.  The lengths
-//    are on the device only; each CTA adds them up itself.  A unit that lies in
-//    one CTA is finished there; otherwise each CTA writes its piece and the last
-//    to arrive (a counter per unit, which it sets back to zero) joins them in the
-//    order of the CTAs, so that the result does not depend on who was last.
+//    are on the device only; each warp adds them up itself.  A unit that lies in
+//    one CTA is finished there; otherwise each CTA writes its piece, and a second
+//    kernel joins the pieces of each row (with a shared prefix's partials, where
+//    there is one), in the order of the CTAs.  (The last CTA of a unit to arrive,
+//    found by a counter, took 3.8 us from its piece to O; the second kernel, which
+//    is resident and waiting by then, takes about 2.)
 //  - Each of a CTA's 4 warps streams its own 16 rows of every granule through
 //    its own ring of 8 KB stages (K and V of 16 rows), so a warp never waits for
 //    another one until the unit ends.  Two CTAs an SM.  Every row: two 2-D boxes
@@ -48,7 +50,7 @@ constexpr int kPgGranule = kPgWarps * kPageRows;   // rows
 constexpr int kPgHalf = kPageRows * 128;           // 64 elements of 16 rows: 2 KB
 constexpr int kPgStage = 4 * kPgHalf;              // K halves, V halves: 8 KB
 constexpr int kPgCtasPerSm = 2;
-constexpr int kPgPieces = 16;  // pieces of a unit that one round of loads joins
+constexpr int kPgPieces = 64;  // pieces of a unit that one round of loads joins
 constexpr int kPgLong = 8;     // granules a CTA above which more pieces pay
 constexpr float kNegInf = -INFINITY;
 
@@ -56,15 +58,27 @@ template <int NT>
 struct PgCfg {
     static constexpr int kStages = NT == 1 ? 3 : 2;
     static constexpr int kHeads = NT * 8;
-    // all of it dynamic (1024-byte aligned): rings, merge buffer, barriers and scalars.
-    // Two CTAs of 115,360 B (one n-tile) and their 1 KB each fit an SM's 228 KB.
+    // all of it dynamic (1024-byte aligned): rings, merge buffer, barriers.
+    // Two CTAs of 115,296 B (one n-tile) and their 1 KB each fit an SM's 228 KB.
     static constexpr int kMerge = kPgWarps * kStages * kPgStage;
     static constexpr int kBars = kMerge + kPgWarps * kHeads * kPartFloats * 4;
-    static constexpr int kScan = kBars + kPgWarps * kStages * 8;
-    static constexpr int kSmem = kScan + kPgWarps * 8 + 32;
+    static constexpr int kSmem = kBars + kPgWarps * kStages * 8;
 };
 
 int paged_ctas() { return kPgCtasPerSm * kPagedSms; }
+
+// n granules over nc CTAs: the first n % nc take one more
+struct Shares {
+    int n, nc, each, more;
+    __device__ __forceinline__ Shares(int n_, int nc_) : n(n_), nc(nc_), each(0), more(0) {
+        if (nc > 0) each = n / nc, more = n - each * nc;
+    }
+    __device__ __forceinline__ int start(int c) const { return c * each + min(c, more); }
+    __device__ __forceinline__ int cta_of(int x) const {
+        const int wide = more * (each + 1);
+        return x < wide ? x / (each + 1) : more + (x - wide) / each;
+    }
+};
 
 // Where a sequence's rows begin and end for this pass, in granules of 64 rows.
 struct Span {
@@ -83,7 +97,7 @@ struct PgArgs {
     uint16_t* O;
     float* lse;
     float* pieces;       // [2 * gridDim.x][G][kPartFloats]
-    unsigned* counters;  // [B * Hkv], zero between calls
+    int2* units;         // [B * Hkv]: a unit's first piece and their number (0: the CTA that holds it wrote its rows)
     PrefixParts pre;
     float* own;          // over a shared prefix: [B][Hq][kPartFloats], where this pass's partials go
     unsigned* flag;
@@ -228,10 +242,6 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     using Cfg = PgCfg<NT>;
     extern __shared__ __align__(1024) unsigned char pg_smem[];
     uint64_t* s_full = reinterpret_cast<uint64_t*>(pg_smem + Cfg::kBars);  // per warp and stage
-    long long* s_scan = reinterpret_cast<long long*>(pg_smem + Cfg::kScan);
-    long long& s_base = s_scan[kPgWarps];
-    int& s_b = reinterpret_cast<int*>(s_scan + kPgWarps + 1)[0];
-    int& s_last = reinterpret_cast<int*>(s_scan + kPgWarps + 1)[1];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
     unsigned char* ringp = pg_smem + warp * Cfg::kStages * kPgStage;
     const unsigned ring = su32(ringp);
@@ -244,52 +254,51 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     // nothing is read here, and which has waited for the kernel before it.
     if (a.pre.splits == 0) griddep_wait();
 
-    // ---- the CTA's share: granules [g0, g1) of all units' laid end to end
+    griddep_launch();  // the joining kernel may take its place (it waits for this one's end)
+
+    // ---- the CTA's share: granules [g0, g1) of all units' laid end to end.  Every
+    // warp adds up the lengths, four sequences a lane at a time (up to 128
+    // sequences: all at once, and the second pass finds them in registers)
     const int B = a.c.B, Hkv = a.c.Hkv;
-    auto block_sum = [&](long long v, long long* before) {  // sum over the CTA; *before: of the lower threads
-        long long inc = v;
+    int cnt[4], total = 0;
+    auto counts = [&](int b0, bool report) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int b = b0 + lane * 4 + k;
+            cnt[k] = b < B ? span_of<GATHER>(a, b, report).granules() * Hkv : 0;
+        }
+        return cnt[0] + cnt[1] + cnt[2] + cnt[3];
+    };
+    for (int b0 = 0; b0 < B; b0 += 128) total += __reduce_add_sync(0xffffffffu, counts(b0, cta == 0 && warp == 0));
+    // CTAs with work.  Few units are not spread over more CTAs than it takes to read
+    // them: joining a unit's pieces costs a round trip for each kPgPieces of them.
+    const Shares share(total, (int)min((long long)min((int)gridDim.x, total), max((long long)B * Hkv * kPgPieces, (long long)total / kPgLong)));
+    const int g0 = cta < share.nc ? share.start(cta) : 0, g1 = cta < share.nc ? share.start(cta + 1) : 0;
+    int first_b = 0, first_base = 0;  // the sequence that holds granule g0, and its first granule
+    for (int b0 = 0, run = 0; b0 < B && g0 < g1; b0 += 128) {
+        const int sum = B > 128 ? counts(b0, false) : cnt[0] + cnt[1] + cnt[2] + cnt[3];
+        int at = sum;
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
-            const long long o = __shfl_up_sync(0xffffffffu, inc, m);
-            if (lane >= m) inc += o;
+            const int o = __shfl_up_sync(0xffffffffu, at, m);
+            if (lane >= m) at += o;
         }
-        __syncthreads();
-        if (lane == 31) s_scan[warp] = inc;
-        __syncthreads();
-        long long pre = 0, tot = 0;
-        for (int w = 0; w < kPgWarps; ++w) {
-            if (w < warp) pre += s_scan[w];
-            tot += s_scan[w];
+        const int all = __shfl_sync(0xffffffffu, at, 31);
+        at += run - sum;  // before this lane's four
+        int fb = -1, base = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (cnt[k] > 0 && at <= g0 && g0 < at + cnt[k]) fb = b0 + lane * 4 + k, base = at;
+            at += cnt[k];
         }
-        *before = pre + inc - v;
-        return tot;
-    };
-    long long total = 0, before, mine = 0;  // (up to kPgThreads sequences: one scan serves for both)
-    for (int b0 = 0; b0 < B; b0 += kPgThreads) {
-        const int b = b0 + tid;
-        mine = b < B ? (long long)span_of<GATHER>(a, b, cta == 0).granules() * Hkv : 0;
-        total += block_sum(mine, &before);
+        const unsigned who = __ballot_sync(0xffffffffu, fb >= 0);
+        if (who) {
+            first_b = __shfl_sync(0xffffffffu, fb, __ffs(who) - 1);
+            first_base = __shfl_sync(0xffffffffu, base, __ffs(who) - 1);
+            break;
+        }
+        run += all;
     }
-    // CTAs with work.  Few units are not spread over more CTAs than it takes to read
-    // them: joining a unit's pieces costs a round trip for each 16 of them.
-    const long long nc = min(min((long long)gridDim.x, total), max((long long)B * Hkv * kPgPieces, total / kPgLong));
-    const long long g0 = cta < nc ? total * cta / nc : 0, g1 = cta < nc ? total * (cta + 1) / nc : 0;
-    long long run = 0;
-    for (int b0 = 0; b0 < B && g0 < g1; b0 += kPgThreads) {  // which sequence holds granule g0
-        const int b = b0 + tid;
-        long long t = total;
-        if (B > kPgThreads) {
-            mine = b < B ? (long long)span_of<GATHER>(a, b, false).granules() * Hkv : 0;
-            t = block_sum(mine, &before);
-        }
-        if (mine > 0 && run + before <= g0 && g0 < run + before + mine) {
-            s_b = b;
-            s_base = run + before;
-        }
-        run += t;
-        if (run > g0) break;
-    }
-    __syncthreads();
 
     if (g0 < g1) {
         auto enter = [&](Cursor& c) {  // c.b is set: the span, its first granule
@@ -311,16 +320,28 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             return true;
         };
         Cursor at;  // of the consumer
-        at.b = s_b;
+        at.b = first_b;
         enter(at);
-        {
-            const long long off = g0 - s_base;
-            const int n = at.s.granules();
-            at.h = (int)(off / n);
-            at.x += (int)(off - (long long)at.h * n);
-        }
+        at.h = (g0 - first_base) / at.s.granules();
+        at.x += g0 - first_base - at.h * at.s.granules();
         Cursor ld = at;  // of the loads
-        const int total_g = (int)(g1 - g0);
+        const int total_g = g1 - g0;
+
+        // ---- the products' operand of the unit at hand (its loads are issued before its rows')
+        uint32_t qf[NT][8][2];
+        auto load_q = [&] {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const int head = t * 8 + (lane >> 2);
+                const uint16_t* qp = a.Q + ((long long)at.b * a.Hq + at.h * a.G + head) * kD + (lane & 3) * 2;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    qf[t][k][0] = head < a.G ? *reinterpret_cast<const uint32_t*>(qp + k * 16) : 0u;
+                    qf[t][k][1] = head < a.G ? *reinterpret_cast<const uint32_t*>(qp + k * 16 + 8) : 0u;
+                }
+            }
+        };
+        load_q();
 
         // ---- the loads.  Every row: lane i keeps the page of this warp's tile of
         // granule pg_x + i.  A tile that is not there (no row of the sequence in
@@ -411,7 +432,6 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         for (int i = 0; i < Cfg::kStages; ++i) issue_next(i);
 
         // ---- the products
-        uint32_t qf[NT][8][2];
         float acc[NT][8][4], m[NT][2], l[NT][2];
         bool open = false;  // a unit is being summed
         int seg0 = 0;       // its first granule here
@@ -419,15 +439,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             if (!open) {
                 open = true;
                 seg0 = at.x;
+                if (i > 0) load_q();
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    const int head = t * 8 + (lane >> 2);
-                    const uint16_t* qp = a.Q + ((long long)at.b * a.Hq + at.h * a.G + head) * kD + (lane & 3) * 2;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        qf[t][k][0] = head < a.G ? *reinterpret_cast<const uint32_t*>(qp + k * 16) : 0u;
-                        qf[t][k][1] = head < a.G ? *reinterpret_cast<const uint32_t*>(qp + k * 16 + 8) : 0u;
-                    }
 #pragma unroll
                     for (int k = 0; k < 8; ++k) acc[t][k][0] = acc[t][k][1] = acc[t][k][2] = acc[t][k][3] = 0.f;
                     m[t][0] = m[t][1] = kNegInf;
@@ -469,16 +483,18 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                         __syncwarp();
                     }
                 }
-                float s[NT][4];
+                float s[NT][4], s2[NT][4];  // two chains of products
 #pragma unroll
-                for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[t][j] = s2[t][j] = 0.f;
                 const int fr = lane & 15, fc = lane >> 4;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     uint32_t kf[4];
                     ldsm4(kf, st + (k >> 2) * kPgHalf + fr * 128 + ((((k & 3) * 2 + fc) ^ (fr & 7)) << 4));
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) E::mma(s[t], kf, qf[t][k][0], qf[t][k][1]);
+                    for (int t = 0; t < NT; ++t) E::mma(k & 1 ? s2[t] : s[t], kf, qf[t][k][0], qf[t][k][1]);
                 }
                 const int row = lane >> 2;
                 const bool v0 = valid >> row & 1u, v1 = valid >> (row + 8) & 1u;
@@ -486,7 +502,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) s[t][j] = (j < 2 ? v0 : v1) ? s[t][j] * a.scale_log2 : kNegInf;
+                    for (int j = 0; j < 4; ++j) s[t][j] = (j < 2 ? v0 : v1) ? (s[t][j] + s2[t][j]) * a.scale_log2 : kNegInf;
                     up |= fmaxf(s[t][0], s[t][2]) > m[t][0] || fmaxf(s[t][1], s[t][3]) > m[t][1];
                 }
                 if (__any_sync(0xffffffffu, up)) {  // a larger maximum: rescale what there is
@@ -566,11 +582,14 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                 }
             }
             __syncthreads();
-            // the unit's granules laid end to end: [u0, u1)
             const bool whole = seg0 == cur.s.first() && cur.x + 1 == cur.hi;
-            const long long gend = g0 + i + 1, u1 = gend + (cur.hi - cur.x - 1), u0 = u1 - cur.s.granules();
-            const long long c0 = ((u0 + 1) * nc - 1) / total, c1 = (u1 * nc - 1) / total;  // its CTAs
+            const int u0 = g0 + i - (cur.x - cur.s.first());  // the unit's first granule, laid end to end
+            // a CTA's pieces: of the unit it begins in, then of the unit it ends in
             float* piece = a.pieces + (2LL * cta + (u0 > g0 ? 1 : 0)) * a.G * kPartFloats;
+            if (tid == 0 && u0 >= g0) {  // the unit begins here
+                const int c1 = share.cta_of(u0 + cur.s.granules() - 1);
+                a.units[(long long)cur.b * Hkv + cur.h] = make_int2(2 * cta + (u0 > g0 ? 1 : 0), whole ? 0 : c1 - cta + 1);
+            }
             for (int g = warp; g < a.G; g += kPgWarps) {
                 float M = kNegInf, L = 0.f, f[kPgWarps];
                 const float* w = merge + g * kPartFloats;
@@ -598,34 +617,6 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                     if (lane == 0) __stcg(reinterpret_cast<float2*>(p + kD), make_float2(M, L));
                 }
             }
-            if (!whole) {
-                __threadfence();
-                __syncthreads();
-                if (tid == 0) {
-                    const unsigned n = (unsigned)(c1 - c0 + 1);
-                    unsigned* cnt = a.counters + (long long)cur.b * Hkv + cur.h;
-                    const unsigned old = atomicAdd(cnt, 1u);
-                    if (old + 1 == n) *cnt = 0u;
-                    s_last = old + 1 == n;
-                }
-                __syncthreads();
-                if (s_last) {
-                    __threadfence();
-                    const int n = (int)(c1 - c0 + 1);
-                    for (int g = warp; g < a.G; g += kPgWarps) {
-                        auto part = [&](int k) -> const float* {
-                            const long long c = c0 + k;
-                            const bool second = k == 0 && u0 > total * c / nc;
-                            return a.pieces + ((2 * c + (second ? 1 : 0)) * a.G + g) * kPartFloats;
-                        };
-                        float M, L;
-                        float* wts = merge + g * n;
-                        const float4 o = join_sums(n, 0, 1, part, wts, lane,
-                                                   [&] { join_weights(n, part, wts, lane, &M, &L); });
-                        put_row<E>(a, (long long)cur.b * a.Hq + cur.h * a.G + g, o, M, L, lane);
-                    }
-                }
-            }
             __syncthreads();  // the merge buffer is free again
         }
         if (GATHER) cp_async_wait<0>();
@@ -634,37 +625,44 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             if (pending >> i & 1u) mbar_wait(su32(&s_full[warp * Cfg::kStages + i]), phase >> i & 1u, nullptr);
     }
 
-    // ---- sequences without a row (of their own)
-    for (int b = cta; b < B; b += gridDim.x) {
-        if (span_of<GATHER>(a, b, false).granules() > 0) continue;
-        for (int r = warp; r < a.Hq; r += kPgWarps)
-            put_row<E>(a, (long long)b * a.Hq + r, make_float4(0.f, 0.f, 0.f, 0.f), kNegInf, 0.f, lane);
-    }
     if (a.pre.splits > 0) griddep_wait();  // the prefix's pass is over before this one counts as over
-    griddep_launch();
 }
 
-// Over a shared prefix: every row's partials (the prefix's splits, where the
-// sequence holds the prefix whole, and its own rows' one) into O and lse.  W warps
-// a row, each with a part of the partials, whose loads are all on their way at once.
+// Every row's partials into O and lse: a shared prefix's (one of each split, where
+// the sequence holds the prefix whole), and the pieces of its own rows.  A row
+// whose unit lay in one CTA, without a prefix, is in O already; a sequence without a
+// row gets zeros.  W warps a row, each with a part of the partials, whose loads are
+// all on their way at once.
 constexpr int kJoinWarps = 4;
-template <class E, int W>
+constexpr int kMaxPieces = kPgCtasPerSm * kPagedSms;
+template <class E, int W, bool GATHER>
 __global__ void __launch_bounds__(32 * kJoinWarps)
-prefix_join_kernel(const PgArgs a, int rows) {
-    __shared__ float wts[kJoinWarps][kMaxPrefixSplits + 1];
+paged_join_kernel(const PgArgs a, int rows) {
+    __shared__ float wts[kJoinWarps][kMaxPrefixSplits + kMaxPieces];
     __shared__ float4 sums[kJoinWarps][32];
     griddep_wait();
     griddep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = warp % W;
-    const long long row = (long long)blockIdx.x * (kJoinWarps / W) + warp / W;
+    const int row = blockIdx.x * (kJoinWarps / W) + warp / W;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float M = kNegInf, L = 0.f;
-    if (row < rows) {
-        const int n0 = a.lens[row / a.Hq] >= a.pre.prefix_len ? a.pre.splits : 0, n = n0 + 1;
-        auto part = [&](int i) {
-            return i < n0 ? a.pre.parts + ((long long)i * rows + row) * kPartFloats : a.own + row * kPartFloats;
+    bool mine = row < rows;
+    if (mine) {
+        const int b = row / a.Hq, r = row - b * a.Hq, h = r / a.G, g = r - h * a.G;
+        const int2 unit = a.units[(long long)b * a.c.Hkv + h];  // (of no meaning without rows of its own)
+        const Span s = span_of<GATHER>(a, b, false);
+        const int n0 = s.lo > 0 ? a.pre.splits : 0;
+        const bool some = s.granules() > 0, own = some && unit.y == 0;
+        const int n = n0 + (some ? max(unit.y, 1) : 0);
+        auto part = [&](int i) -> const float* {
+            if (i < n0) return a.pre.parts + ((long long)i * rows + row) * kPartFloats;
+            if (own) return a.own + (long long)row * kPartFloats;
+            // the first piece is either of its CTA's, the others are their CTAs' first
+            const int slot = i == n0 ? unit.x : (unit.x / 2 + i - n0) * 2;
+            return a.pieces + ((long long)slot * a.G + g) * kPartFloats;
         };
-        o = join_sums(n, w, W, part, wts[warp], lane, [&] { join_weights(n, part, wts[warp], lane, &M, &L); });
+        mine = !(own && !a.own);
+        if (mine) o = join_sums(n, w, W, part, wts[warp], lane, [&] { join_weights(n, part, wts[warp], lane, &M, &L); });
     }
     if constexpr (W > 1) {
         sums[warp][lane] = o;
@@ -675,10 +673,10 @@ prefix_join_kernel(const PgArgs a, int rows) {
             o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
         }
     }
-    if (row < rows && w == 0) finish_row<E>(a, row, o, M, L, lane);
+    if (mine && w == 0) finish_row<E>(a, row, o, M, L, lane);
 }
 
-template <class E, int W>
+template <class E, int W, bool GATHER>
 static cudaError_t join_launch(const PgArgs& a, cudaStream_t st) {
     const long long rows = (long long)a.c.B * a.Hq, per = kJoinWarps / W;
     cudaLaunchConfig_t cfg = {};
@@ -688,16 +686,17 @@ static cudaError_t join_launch(const PgArgs& a, cudaStream_t st) {
     cudaLaunchAttribute attr[1] = {pdl_attr()};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, prefix_join_kernel<E, W>, a, (int)rows);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_join_kernel<E, W, GATHER>, a, (int)rows);
     note_launch();
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 // Few rows: four warps each (256 rows of 17 partials 3.6 us, against 7.5 with one);
 // many: one each, which fills the SMs (4096 rows of 10: 7.1 us, against 17 with four).
-template <class E>
+template <class E, bool GATHER>
 static cudaError_t join_pick(const PgArgs& a, cudaStream_t st) {
-    return (long long)a.c.B * a.Hq <= 8 * kPagedSms ? join_launch<E, kJoinWarps>(a, st) : join_launch<E, 1>(a, st);
+    return (long long)a.c.B * a.Hq <= 8 * kPagedSms ? join_launch<E, kJoinWarps, GATHER>(a, st)
+                                                    : join_launch<E, 1, GATHER>(a, st);
 }
 
 template <class E, int NT, bool GATHER>
@@ -726,7 +725,7 @@ static cudaError_t paged_pick(int grid, const CUtensorMap& km, const CUtensorMap
 
 cudaError_t launch_paged_attn(const Pages& c, const void* Q, int Hq, const int32_t* lens, const int32_t* idx,
                               const int32_t* kreq, int k_max, float scale, void* O, float* lse, float* pieces,
-                              unsigned* counters, const PrefixParts& pre, unsigned* flag, cudaStream_t st) {
+                              int32_t* units, const PrefixParts& pre, unsigned* flag, cudaStream_t st) {
     if (c.B == 0) return cudaSuccess;
     PgArgs a;
     a.c = c;
@@ -741,7 +740,7 @@ cudaError_t launch_paged_attn(const Pages& c, const void* Q, int Hq, const int32
     a.O = static_cast<uint16_t*>(O);
     a.lse = lse;
     a.pieces = pieces;
-    a.counters = counters;
+    a.units = reinterpret_cast<int2*>(units);
     a.pre = pre;
     a.own = pre.splits > 0 ? pre.own : nullptr;
     a.flag = flag;
@@ -753,8 +752,9 @@ cudaError_t launch_paged_attn(const Pages& c, const void* Q, int Hq, const int32
     }
     const int grid = paged_ctas();
     const cudaError_t e = c.half ? paged_pick<F16>(grid, km, vm, a, st) : paged_pick<Bf16>(grid, km, vm, a, st);
-    if (e != cudaSuccess || pre.splits == 0) return e;
-    return c.half ? join_pick<F16>(a, st) : join_pick<Bf16>(a, st);
+    if (e != cudaSuccess) return e;
+    if (idx) return c.half ? join_pick<F16, true>(a, st) : join_pick<Bf16, true>(a, st);
+    return c.half ? join_pick<F16, false>(a, st) : join_pick<Bf16, false>(a, st);
 }
 
 }  // namespace tsa
