@@ -192,31 +192,33 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     auto count = [&](int s) { return pair ? nt : (nt - s + 1) >> 1; };
     auto tile_of = [&](int s, int i) { return pair ? i : 2 * i + s; };  // (of this CTA's)
 
-    // ---- the producer's loads (warp 17): K of tile t at ring position 2t, V at 2t + 1
+    // ---- the producer's loads (warp 17): K of tile t at ring position 2t, V at 2t + 1.
+    // The lanes hold the pages of the boxes of the next 32 / chunks tiles.
     const unsigned smem0 = su32(px_smem);
     const uint64_t pol = evict_first_policy();
-    int load_pos = 0, load_row = 0, load_page = 0;  // this lane's box of the tile of load_pos
+    int load_pos = 0, pages = 0, pages_t = 0;  // pages of the tiles from pages_t on
+    const int ahead = 32 / chunks;
     auto load_next = [&] {
         const int t = load_pos >> 1, kv = load_pos & 1, chunk = lane >> 1, half = lane & 1;
-        const bool mine = chunk < chunks;
-        if (!kv) {
-            const int r = (t0 + t) * kPxTile + chunk * box, pg = r / a.page_size;
-            load_row = r - pg * a.page_size;
-            load_page = a.num_pages;  // outside the map: zeros
-            if (mine && r < a.prefix_len) {
-                load_page = table[pg];
-                if (load_page < 0 || load_page >= a.num_pages) {
+        if (!kv && (t == 0 || t - pages_t == ahead)) {
+            pages_t = t;
+            const int pt = t + lane / chunks, r = (t0 + pt) * kPxTile + lane % chunks * box;
+            pages = a.num_pages;  // outside the map: zeros
+            if (pt < nt && r < a.prefix_len) {
+                pages = table[r / a.page_size];
+                if (pages < 0 || pages >= a.num_pages) {
                     atomicOr(a.flag, kFlagBounds);
-                    load_page = a.num_pages;
+                    pages = a.num_pages;
                 }
             }
         }
         const int st = load_pos % kPxStages;
         if (lane == 0) mbar_arrive_tx(full(st), kPxStage);
         __syncwarp();
-        if (mine)
+        const int page = __shfl_sync(0xffffffffu, pages, (t - pages_t) * chunks + (chunk < chunks ? chunk : 0));
+        if (chunk < chunks)
             tma_4d(smem0 + kPxRing + st * kPxStage + half * kPxHalf + chunk * box * 128, kv ? &vmap : &kmap, half * 64,
-                   load_row, h, load_page, full(st), pol);
+                   ((t0 + t) * kPxTile + chunk * box) % a.page_size, h, page, full(st), pol);
         ++load_pos;
     };
 
@@ -241,7 +243,8 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             mbar_init_fence();
         }
         __syncwarp();
-        while (load_pos < 2 * nt && load_pos < kPxStages) load_next();  // the ring is empty: nothing to wait for
+        load_next();  // the first tile's (the ring is empty: nothing to wait for)
+        load_next();
     } else if (warp < kPxSoftWarps) {  // Q: row r of stream s at half * 16 KB + r * 128 B, 16-byte chunks swizzled; rows past R are zeros
         // (all of a thread's loads are in flight at once)
         const int c = tid & 15;
@@ -272,7 +275,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         // ---- TMA producer
         bool ok = true;
         while (load_pos < 2 * nt) {
-            ok = __all_sync(0xffffffffu, mbar_wait(empty(load_pos % kPxStages), (load_pos / kPxStages - 1) & 1, a.flag));
+            if (load_pos >= kPxStages) ok = __all_sync(0xffffffffu, mbar_wait(empty(load_pos % kPxStages), (load_pos / kPxStages - 1) & 1, a.flag));
             if (!ok) break;
             load_next();
         }
