@@ -172,6 +172,36 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 2 * kPxStages + 10);
     const int box_log = 4 + a.box_log, box = 1 << box_log, chunks = kPxTile >> box_log;
 
+    const int grp = blockIdx.x % a.groups, h = blockIdx.x / a.groups % a.Hkv, split = blockIdx.x / (a.groups * a.Hkv);
+    const int nt_all = (a.prefix_len + kPxTile - 1) / kPxTile;  // (2^23 at most, 128 splits)
+    const int t0 = nt_all * split / a.splits, nt = nt_all * (split + 1) / a.splits - t0;
+    const int R = a.B * a.G, row0 = grp * kPxRows;
+    const bool pair = R - row0 > kPxTile;  // two streams of rows; else two streams of tiles
+    // set-up that touches no memory of the caller's: before the wait on the kernel before
+    if (warp == 16) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(su32(s_tmem)),
+                     "r"(kPxTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+    } else if (warp == 17) {
+        if (lane == 0) {
+            asm volatile("prefetch.tensormap [%0];\n" ::"l"(&kmap) : "memory");
+            asm volatile("prefetch.tensormap [%0];\n" ::"l"(&vmap) : "memory");
+            for (int i = 0; i < kPxStages; ++i) {
+                mbar_init(full(i), 1);
+                mbar_init(empty(i), pair ? 2 : 1);  // the streams that use a tile
+            }
+            for (int s = 0; s < 2; ++s) {
+                mbar_init(sfull(s), 1);
+                mbar_init(pfull(s), 2 * kPxTile);
+                mbar_init(ofull(s), 1);
+                mbar_init(drain(s), 1);
+                mbar_init(turn(s), 1);
+            }
+            mbar_init_fence();
+        }
+        __syncwarp();
+    }
     griddep_wait();
     griddep_launch();  // the pass over the sequences' own rows reads nothing of this one
     // the sequence through whose table the prefix is read: the first that holds it whole
@@ -180,13 +210,12 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         const unsigned v = __ballot_sync(0xffffffffu, b0 + lane < a.B && a.lens[b0 + lane] >= a.prefix_len);
         if (v) src = b0 + __ffs(v) - 1;
     }
-    if (src < 0) return;  // nobody does: uniform, before any barrier or TMEM
-
-    const int grp = blockIdx.x % a.groups, h = blockIdx.x / a.groups % a.Hkv, split = blockIdx.x / (a.groups * a.Hkv);
-    const int nt_all = (a.prefix_len + kPxTile - 1) / kPxTile;
-    const int t0 = (int)((long long)nt_all * split / a.splits), nt = (int)((long long)nt_all * (split + 1) / a.splits) - t0;
-    const int R = a.B * a.G, row0 = grp * kPxRows;
-    const bool pair = R - row0 > kPxTile;  // two streams of rows; else two streams of tiles
+    if (src < 0) {  // nobody does
+        __syncthreads();
+        if (warp == 16)
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(*s_tmem), "r"(kPxTmemCols) : "memory");
+        return;
+    }
     const int32_t* table = a.table + (long long)src * a.width;
     // the tiles of stream s: all of the split's, or every other one
     auto count = [&](int s) { return pair ? nt : (nt - s + 1) >> 1; };
@@ -222,27 +251,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         ++load_pos;
     };
 
-    if (warp == 16) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(su32(s_tmem)),
-                     "r"(kPxTmemCols)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
-    } else if (warp == 17) {
-        if (lane == 0) {
-            for (int i = 0; i < kPxStages; ++i) {
-                mbar_init(full(i), 1);
-                mbar_init(empty(i), pair ? 2 : 1);  // the streams that use a tile
-            }
-            for (int s = 0; s < 2; ++s) {
-                mbar_init(sfull(s), 1);
-                mbar_init(pfull(s), 2 * kPxTile);
-                mbar_init(ofull(s), 1);
-                mbar_init(drain(s), 1);
-                mbar_init(turn(s), 1);
-            }
-            mbar_init_fence();
-        }
-        __syncwarp();
+    if (warp == 17) {
         load_next();  // the first tile's (the ring is empty: nothing to wait for)
         load_next();
     } else if (warp < kPxSoftWarps) {  // Q: row r of stream s at half * 16 KB + r * 128 B, 16-byte chunks swizzled; rows past R are zeros
