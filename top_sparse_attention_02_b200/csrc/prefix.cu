@@ -56,9 +56,8 @@ constexpr int kPxRing = 2 * kPxStage;
 constexpr int kPxBars = kPxRing + kPxStages * kPxStage;
 constexpr int kPxMax = kPxBars + 256;            // the halves' maxima: [stream][half][row]
 constexpr int kPxSmem = kPxMax + 2 * 2 * kPxTile * 4;
-constexpr int kPxJoinStride = kD + 4;         // floats of a row handed from stream 1 to stream 0
 constexpr int kPxTmemCols = 512;
-static_assert(kPxTile * kPxJoinStride * 4 <= kPxStages * kPxStage, "the rows handed over fit the ring");
+static_assert(kPxRows * kPartFloats * 4 <= kPxStages * kPxStage, "the rows' partials fit the ring");
 
 struct PxArgs {
     const uint16_t* Q;
@@ -204,6 +203,23 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     }
     griddep_wait();
     griddep_launch();  // the pass over the sequences' own rows reads nothing of this one
+    // What needs no length is requested first: Q (all of a thread's loads at once;
+    // rows past R are zeros), and the first tiles' pages as the first sequence has them.
+    uint4 qv[kPxRows / 32];
+    int pages = 0;
+    const int ahead = 32 / chunks;  // tiles whose pages the producer's lanes hold
+    if (warp < kPxSoftWarps) {
+#pragma unroll
+        for (int i = 0; i < kPxRows / 32; ++i) {
+            const int gr = row0 + i * 32 + (tid >> 4), b = gr / a.G;
+            qv[i] = make_uint4(0, 0, 0, 0);
+            if (gr < R)
+                qv[i] = *reinterpret_cast<const uint4*>(a.Q + ((long long)b * a.Hq + h * a.G + gr - b * a.G) * kD + (tid & 15) * 8);
+        }
+    } else if (warp == 17) {
+        const int r = (t0 + lane / chunks) * kPxTile + lane % chunks * box;
+        if (lane / chunks < nt && r < a.prefix_len) pages = a.table[r / a.page_size];
+    }
     // the sequence through whose table the prefix is read: the first that holds it whole
     int src = -1;
     for (int b0 = 0; b0 < a.B && src < 0; b0 += 32) {
@@ -225,20 +241,20 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     // The lanes hold the pages of the boxes of the next 32 / chunks tiles.
     const unsigned smem0 = su32(px_smem);
     const uint64_t pol = evict_first_policy();
-    int load_pos = 0, pages = 0, pages_t = 0;  // pages of the tiles from pages_t on
-    const int ahead = 32 / chunks;
+    int load_pos = 0, pages_t = 0;  // (pages: of the tiles from pages_t on)
     auto load_next = [&] {
         const int t = load_pos >> 1, kv = load_pos & 1, chunk = lane >> 1, half = lane & 1;
         if (!kv && (t == 0 || t - pages_t == ahead)) {
             pages_t = t;
             const int pt = t + lane / chunks, r = (t0 + pt) * kPxTile + lane % chunks * box;
-            pages = a.num_pages;  // outside the map: zeros
             if (pt < nt && r < a.prefix_len) {
-                pages = table[r / a.page_size];
+                if (t > 0 || src > 0) pages = table[r / a.page_size];
                 if (pages < 0 || pages >= a.num_pages) {
                     atomicOr(a.flag, kFlagBounds);
                     pages = a.num_pages;
                 }
+            } else {
+                pages = a.num_pages;  // outside the map: zeros
             }
         }
         const int st = load_pos % kPxStages;
@@ -254,21 +270,13 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     if (warp == 17) {
         load_next();  // the first tile's (the ring is empty: nothing to wait for)
         load_next();
-    } else if (warp < kPxSoftWarps) {  // Q: row r of stream s at half * 16 KB + r * 128 B, 16-byte chunks swizzled; rows past R are zeros
-        // (all of a thread's loads are in flight at once)
+    } else if (warp < kPxSoftWarps) {  // Q: row r of stream s at half * 16 KB + r * 128 B, 16-byte chunks swizzled
         const int c = tid & 15;
-        uint4 v[kPxRows / 32];
-#pragma unroll
-        for (int i = 0; i < kPxRows / 32; ++i) {
-            const int gr = row0 + i * 32 + (tid >> 4), b = gr / a.G;
-            v[i] = make_uint4(0, 0, 0, 0);
-            if (gr < R) v[i] = *reinterpret_cast<const uint4*>(a.Q + ((long long)b * a.Hq + h * a.G + gr - b * a.G) * kD + c * 8);
-        }
 #pragma unroll
         for (int i = 0; i < kPxRows / 32; ++i) {
             const int r = i * 32 + (tid >> 4), rr = r & (kPxTile - 1);
             *reinterpret_cast<uint4*>(px_smem + kPxQ + (r >> 7) * kPxStage + (c >> 3) * kPxHalf + rr * 128 +
-                                      (((c & 7) ^ (rr & 7)) << 4)) = v[i];
+                                      (((c & 7) ^ (rr & 7)) << 4)) = qv[i];
         }
         fence_proxy_async();
     }
@@ -453,65 +461,61 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         maxima[hf * kPxTile + row] = l;
         asm volatile("bar.sync %0, 256;\n" ::"r"(2 + s) : "memory");
         l = maxima[row] + maxima[kPxTile + row];
-        float* join = reinterpret_cast<float*>(px_smem + kPxRing);
-        if (!pair) {  // stream 1 hands its rows to stream 0
-            asm volatile("bar.sync 1, 512;\n" ::: "memory");  // no product reads the ring any more
-            if (s == 1 && ok) {
-#pragma unroll 1
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t o[32];
-                    if (n > 0) {
-                        tm_ld32(o, to + c * 32);
-                        tm_wait_ld();
-                    }
-#pragma unroll
-                    for (int j = 0; j < 32; j += 4)
-                        *reinterpret_cast<uint4*>(join + row * kPxJoinStride + hf * 64 + c * 32 + j) =
-                            n > 0 ? make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]) : make_uint4(0, 0, 0, 0);
-                }
-                if (hf == 0) {
-                    join[row * kPxJoinStride + kD] = m;
-                    join[row * kPxJoinStride + kD + 1] = l;
-                }
-            }
-            asm volatile("bar.sync 1, 512;\n" ::: "memory");
-        }
-        const int gr = row0 + (pair ? s * kPxTile : 0) + row;
-        if (ok && (pair || s == 0)) {
-            const int b = gr / a.G, j = gr - b * a.G;
-            float* out = a.parts + (((long long)split * a.B + b) * a.Hq + h * a.G + j) * kPartFloats;
-            float f0 = 1.f, f1 = 0.f;
-            const float* other = join + row * kPxJoinStride;
-            if (!pair) {
-                const float m1 = other[kD], l1 = other[kD + 1], M = fmaxf(m, m1);
-                f0 = m == -INFINITY ? 0.f : ex2(m - M);
-                f1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
-                l = (m == -INFINITY ? l : f0 * l) + (m1 == -INFINITY ? l1 : f1 * l1);
-                m = M;
-            }
+        // The rows' partials are put together in the ring, 528 B each as in memory, and
+        // copied out by the copy engine.  (Written from the registers, 16 B a row at a
+        // time, they took 2.5 us.)  Without a second stream's rows, stream 1 hands its to stream 0.
+        asm volatile("bar.sync 1, 512;\n" ::: "memory");  // no product reads the ring any more
+        unsigned char* out = px_smem + kPxRing + (pair ? s * kPxTile * kPartFloats * 4 : 0);
+        float* mine = reinterpret_cast<float*>(out) + row * kPartFloats;
+        if (ok && (pair || s == 1)) {
 #pragma unroll 1
             for (int c = 0; c < 2; ++c) {
                 uint32_t o[32];
-                tm_ld32(o, to + c * 32);
-                tm_wait_ld();
-                if (gr < R) {
+                if (n > 0) {
+                    tm_ld32(o, to + c * 32);
+                    tm_wait_ld();
+                }
 #pragma unroll
-                    for (int k = 0; k < 32; k += 4) {
-                        float4 v = make_float4(__uint_as_float(o[k]), __uint_as_float(o[k + 1]), __uint_as_float(o[k + 2]),
-                                               __uint_as_float(o[k + 3]));
-                        if (!pair) {
-                            const float4 w = *reinterpret_cast<const float4*>(other + hf * 64 + c * 32 + k);
-                            v.x = f0 * v.x + f1 * w.x, v.y = f0 * v.y + f1 * w.y;
-                            v.z = f0 * v.z + f1 * w.z, v.w = f0 * v.w + f1 * w.w;
-                        }
-                        *reinterpret_cast<float4*>(out + hf * 64 + c * 32 + k) = v;
+                for (int j = 0; j < 32; j += 4)
+                    *reinterpret_cast<uint4*>(mine + hf * 64 + c * 32 + j) =
+                        n > 0 ? make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]) : make_uint4(0, 0, 0, 0);
+            }
+            if (hf == 0) *reinterpret_cast<float4*>(mine + kD) = make_float4(m, l, 0.f, 0.f);
+        }
+        if (!pair) {
+            asm volatile("bar.sync 1, 512;\n" ::: "memory");
+            const float m1 = mine[kD], l1 = mine[kD + 1], M = fmaxf(m, m1);
+            const float f0 = m == -INFINITY ? 0.f : ex2(m - M), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
+            if (ok && s == 0) {
+#pragma unroll 1
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t o[32];
+                    tm_ld32(o, to + c * 32);
+                    tm_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) {
+                        float4* w = reinterpret_cast<float4*>(mine + hf * 64 + c * 32 + j);
+                        float4 v = *w;
+                        v.x = fmaf(f1, v.x, f0 * __uint_as_float(o[j])), v.y = fmaf(f1, v.y, f0 * __uint_as_float(o[j + 1]));
+                        v.z = fmaf(f1, v.z, f0 * __uint_as_float(o[j + 2])), v.w = fmaf(f1, v.w, f0 * __uint_as_float(o[j + 3]));
+                        *w = v;
                     }
                 }
+                l = (m == -INFINITY ? l : f0 * l) + (m1 == -INFINITY ? l1 : f1 * l1);
             }
-            if (gr < R && hf == 0) {
-                out[kD] = m;
-                out[kD + 1] = l;
+            asm volatile("bar.sync %0, 256;\n" ::"r"(2 + s) : "memory");  // both halves have read the other's m and l
+            if (ok && s == 0 && hf == 0) *reinterpret_cast<float2*>(mine + kD) = make_float2(M, l);
+        }
+        fence_proxy_async();
+        asm volatile("bar.sync %0, 256;\n" ::"r"(2 + s) : "memory");
+        if (ok && (pair || s == 0)) {  // a sequence's rows of this head are contiguous: one copy each
+            const int lo = row0 + (pair ? s * kPxTile : 0), hi = min(lo + kPxTile, R), b0 = lo / a.G;
+            for (int b = b0 + (tid & 255); b * a.G < hi; b += 256) {
+                const int r0 = max(b * a.G, lo), r1 = min((b + 1) * a.G, hi);
+                bulk_store(a.parts + (((long long)split * a.B + b) * a.Hq + h * a.G + r0 - b * a.G) * kPartFloats,
+                           su32(out) + (r0 - lo) * kPartFloats * 4, (r1 - r0) * kPartFloats * 4);
             }
+            bulk_store_wait();
         }
     }
     tc_fence_before();

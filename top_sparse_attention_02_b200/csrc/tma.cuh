@@ -64,6 +64,15 @@ __device__ __forceinline__ void tma_4d(unsigned dst, const CUtensorMap* map, int
 
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
 
+// contiguous bytes (a multiple of 16, 16-byte aligned) out of shared memory; then wait until they are in memory
+__device__ __forceinline__ void bulk_store(void* dst, unsigned src, int bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_store_wait() {
+    asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
+    asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
+}
+
 // 16 bytes into shared memory, the last 16 - n of them zeros
 __device__ __forceinline__ void cp_async16(unsigned dst, const void* src, int n) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(n) : "memory");
