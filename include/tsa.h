@@ -412,7 +412,7 @@ tsa_status tsa_paged_append(const tsa_append_args* args, void* stream);
 
 /* Bytes of workspace that tsa_paged_attn (prefix_len = 0) or tsa_prefix_attn needs for
  * this cache and Hq query heads; Hq = 0: what tsa_paged_append needs.  A larger
- * prefix_len never needs less.  Returns 0 on invalid arguments.  Zero it once with
+ * prefix_len (up to the table's rows) never needs less.  Returns 0 on invalid arguments.  Zero it once with
  * tsa_workspace_init; the calls leave it ready for the next.  The two calls may
  * share one; calls that share one must be ordered on one stream.  (It is not laid
  * out as tsa_workspace_size's: do not share it with tsa_decode_step.) */
@@ -442,8 +442,11 @@ tsa_status tsa_paged_attn(const tsa_paged_attn_args* args, void* stream);
  * same prefix_len rows: the prefix's K and V are read once for all sequences that
  * hold it whole (len_b >= prefix_len), through the table of the first of them; what
  * follows is read through each sequence's own table.  A sequence shorter than the
- * prefix (or a padding slot with len_b = 0) is attended through its own table alone.
- * The result is tsa_paged_attn's, up to rounding.  prefix_len = 0: no shared rows. */
+ * prefix (or a padding slot with len_b = 0) is attended through its own table alone,
+ * and so is every sequence where the prefix is too short, or the batch too small, for
+ * a pass of its own to pay: every sequence's table names its prefix's pages, too
+ * (shared or copies of one another).  The result is tsa_paged_attn's, up to rounding.
+ * prefix_len = 0: no shared rows; at most 2^30. */
 tsa_status tsa_prefix_attn(const tsa_paged_attn_args* args, void* stream);
 
 /* ------------------------------------------------------------------ status */

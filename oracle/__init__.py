@@ -301,8 +301,9 @@ def norm_rope(x: torch.Tensor, weight, eps: float, positions, inv_freq, interlea
 def paged_rows(pages: torch.Tensor, table, b: int, rows) -> np.ndarray:
     """Rows of sequence b out of pages [num_pages, Hkv, page_size, d]: [Hkv, len(rows), d] float64."""
     size = pages.shape[2]
-    out = [_f64(pages[int(table[b][r // size]), :, r % size]) for r in map(int, rows)]
-    return np.stack(out, 1) if out else np.zeros((pages.shape[1], 0, pages.shape[3]))
+    rows = torch.as_tensor(list(rows), dtype=torch.long)
+    at = torch.as_tensor(table)[b].long().cpu()[rows // size]
+    return _f64(pages[at, :, rows % size].transpose(0, 1))
 
 
 def paged_attn(Q, K_pages, V_pages, table, seq_lens, scale: float, idx=None, k_per_seq=None):

@@ -54,6 +54,12 @@ constexpr int kPgPieces = 64;  // pieces of a unit that one round of loads joins
 constexpr int kPgLong = 8;     // granules a CTA above which more pieces pay
 constexpr float kNegInf = -INFINITY;
 
+#ifdef TSA_DEBUG_KNOBS
+// Debug build only (never in the product library): the granule of CTA 0 whose load
+// warp 0 leaves out, so that the wait on it runs out; -1: none.
+__device__ int g_debug_paged_skip = -1;
+#endif
+
 template <int NT>
 struct PgCfg {
     static constexpr int kStages = NT == 1 ? 3 : 2;
@@ -370,7 +376,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                 }
                 const int page = __shfl_sync(0xffffffffu, pages, ld.x - pg_x);
                 ok = ok && page >= 0;
+#ifdef TSA_DEBUG_KNOBS
+                if (ok && lane == 0 && !(cta == 0 && warp == 0 && ld.x == g_debug_paged_skip)) {
+#else
                 if (ok && lane == 0) {
+#endif
                     const unsigned bar = su32(&s_full[warp * Cfg::kStages + slot]), dst = ring + slot * kPgStage;
                     const int r = r0 % a.c.page_size;
                     mbar_arrive_tx(bar, kPgStage);
@@ -758,3 +768,13 @@ cudaError_t launch_paged_attn(const Pages& c, const void* Q, int Hq, const int32
 }
 
 }  // namespace tsa
+
+#ifdef TSA_DEBUG_KNOBS
+// Debug build only: the granule (0) of the paged attention or the tile (1) of a shared
+// prefix's pass whose load CTA 0 leaves out; -1 for none.  Returns a cudaError_t.
+extern "C" int tsa_debug_prefix_skip_tile(int tile);
+extern "C" int tsa_debug_paged_skip_tile(int which, int tile) {
+    if (which == 1) return tsa_debug_prefix_skip_tile(tile);
+    return (int)cudaMemcpyToSymbol(tsa::g_debug_paged_skip, &tile, sizeof tile);
+}
+#endif

@@ -59,6 +59,12 @@ constexpr int kPxSmem = kPxMax + 2 * 2 * kPxTile * 4;
 constexpr int kPxTmemCols = 512;
 static_assert(kPxRows * kPartFloats * 4 <= kPxStages * kPxStage, "the rows' partials fit the ring");
 
+#ifdef TSA_DEBUG_KNOBS
+// Debug build only (never in the product library): the tile of CTA 0 whose K is neither
+// armed nor loaded, so that the waits on it run out; -1: none.
+__device__ int g_debug_prefix_skip = -1;
+#endif
+
 struct PxArgs {
     const uint16_t* Q;
     const int32_t *lens, *table;
@@ -257,6 +263,12 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
                 pages = a.num_pages;  // outside the map: zeros
             }
         }
+#ifdef TSA_DEBUG_KNOBS
+        if (blockIdx.x == 0 && !kv && t == g_debug_prefix_skip) {
+            ++load_pos;
+            return;
+        }
+#endif
         const int st = load_pos % kPxStages;
         if (lane == 0) mbar_arrive_tx(full(st), kPxStage);
         __syncwarp();
@@ -596,3 +608,9 @@ cudaError_t launch_prefix(const Pages& c, const void* Q, int Hq, const int32_t* 
 }
 
 }  // namespace tsa
+
+#ifdef TSA_DEBUG_KNOBS
+extern "C" int tsa_debug_prefix_skip_tile(int tile) {
+    return (int)cudaMemcpyToSymbol(tsa::g_debug_prefix_skip, &tile, sizeof tile);
+}
+#endif
