@@ -34,10 +34,12 @@ def dbg():
 
 
 # few and many rows of one kv-head: the prefix's pass with one row tile and with two
-@pytest.mark.parametrize("which,B,Hq,tile", [(0, 3, 16, 0), (0, 3, 16, 3), (1, 33, 8, 0), (1, 33, 64, 0), (1, 33, 64, 1)])
-def test_a_wait_runs_out_then_recovers(dbg, cuda_dev, which, B, Hq, tile):
-    P = 400 if which else 0
-    lens = [P + 300 + i for i in range(B)]
+# (P = 4000: 32 tiles in 8 splits, so that CTA 0 has four)
+@pytest.mark.parametrize("which,B,Hq,P,tile", [(0, 3, 16, 0, 0), (0, 3, 16, 0, 3), (1, 33, 8, 400, 0), (1, 33, 64, 400, 0),
+                                               (1, 33, 64, 4000, 1)])
+def test_a_wait_runs_out_then_recovers(dbg, cuda_dev, which, B, Hq, P, tile):
+    # (3 x 8 units of 51 granules over 296 CTAs: five of them, 0 to 4, are CTA 0's)
+    lens = [P + 300 + i for i in range(B)] if which else [3210 + i for i in range(B)]
     K, V, table = pages(lens, 8, 64, torch.bfloat16, seed=1, shared=P, dev=cuda_dev)
     Q = queries(B, Hq, torch.bfloat16, dev=cuda_dev)
     cache = tsa.paged_cache(K, V, table)
