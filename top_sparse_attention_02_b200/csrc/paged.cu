@@ -195,7 +195,7 @@ __device__ __forceinline__ void join_weights(int n, Part part, float* wts, int l
 // weights that join_weights leaves in wts.  kJoinFlight loads are on their way at a
 // time, the first of them before the weights are known (they come out of L2, at
 // about a microsecond a round).
-constexpr int kJoinFlight = 16;
+constexpr int kJoinFlight = 8;
 template <class Part, class Weights>
 __device__ __forceinline__ float4 join_sums(int n, int i0, int step, Part part, const float* wts, int lane, Weights weights) {
     float4 v[kJoinFlight], acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -643,7 +643,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 // whose unit lay in one CTA, without a prefix, is in O already; a sequence without a
 // row gets zeros.  W warps a row, each with a part of the partials, whose loads are
 // all on their way at once.
-constexpr int kJoinWarps = 4;
+constexpr int kJoinWarps = 8;
 constexpr int kMaxPieces = kPgCtasPerSm * kPagedSms;
 template <class E, int W, bool GATHER>
 __global__ void __launch_bounds__(32 * kJoinWarps)
@@ -701,12 +701,15 @@ static cudaError_t join_launch(const PgArgs& a, cudaStream_t st) {
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Few rows: four warps each (256 rows of 17 partials 3.6 us, against 7.5 with one);
-// many: one each, which fills the SMs (4096 rows of 10: 7.1 us, against 17 with four).
+// The fewer rows, the more warps each: 8 (a row of 64 pieces: one round of loads), 4
+// while that fills the SMs once (256 rows of 17 partials 3.6 us, against 7.5 with
+// one), then one (4096 rows of 10: 7.1 us, against 17 with four).
 template <class E, bool GATHER>
 static cudaError_t join_pick(const PgArgs& a, cudaStream_t st) {
-    return (long long)a.c.B * a.Hq <= 8 * kPagedSms ? join_launch<E, kJoinWarps, GATHER>(a, st)
-                                                    : join_launch<E, 1, GATHER>(a, st);
+    const long long rows = (long long)a.c.B * a.Hq;
+    if (rows <= 2 * kPagedSms) return join_launch<E, 8, GATHER>(a, st);
+    if (rows <= 8 * kPagedSms) return join_launch<E, 4, GATHER>(a, st);
+    return join_launch<E, 1, GATHER>(a, st);
 }
 
 template <class E, int NT, bool GATHER>
