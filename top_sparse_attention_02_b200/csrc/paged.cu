@@ -217,6 +217,8 @@ __device__ __forceinline__ float4 join_sums(int n, int i0, int step, Part part, 
     return acc;
 }
 
+__device__ __forceinline__ void prefetch_l1(const void* p) { asm volatile("prefetch.global.L1 [%0];\n" ::"l"(p)); }
+
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], unsigned addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];\n"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -350,29 +352,46 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         load_q();
 
         // ---- the loads.  Every row: lane i keeps the page of this warp's tile of
-        // granule pg_x + i.  A tile that is not there (no row of the sequence in
+        // granule pg_x + i; the sequence's first 32 are kept apart, since each of its
+        // heads begins with them.  A tile that is not there (no row of the sequence in
         // it, or a bad page) is not loaded; `there` says so per stage.
-        int pages = -1, pg_x = 0;
-        bool fresh = true;  // `pages` is of another unit
+        int pages = -1, pg_b = -1, pg_x = 0, head_pages = -1, head_b = -1;
         unsigned there = 0, pending = 0, phase = 0;  // bits of the stages: holds a tile; on its way; barrier's phase
         bool dead = false;                           // a wait gave up: this warp loads and adds no more
         uint64_t pol = evict_first_policy();
+        bool fresh = true;  // (a list) the loads have come to another unit
+        int next_e = -1;    // lane i < 16: entry i of the next tile
+        auto entry = [&](int x) {
+            const int i = x * kPgGranule + warp * kPageRows + lane;
+            return lane < kPageRows && i < ld.s.hi ? a.idx[((long long)ld.b * Hkv + ld.h) * a.k_max + i] : -1;
+        };
+        auto prefetch_q = [&] {  // the unit's queries, G rows of 256 B
+            const int line = lane & 31;
+            if (line < 2 * a.G)
+                prefetch_l1(a.Q + ((long long)ld.b * a.Hq + ld.h * a.G + (line >> 1)) * kD + (line & 1) * 64);
+        };
         auto issue = [&](int slot) {
             const int r0 = ld.x * kPgGranule + warp * kPageRows;  // the tile's first row (or list entry)
             bool ok = r0 < ld.s.hi && r0 + kPageRows > ld.s.lo;
             if constexpr (!GATHER) {
-                if (fresh || ld.x - pg_x >= 32) {
+                if (ld.b != pg_b || ld.x < pg_x || ld.x >= pg_x + 32) {
+                    pg_b = ld.b;
                     pg_x = ld.x;
-                    const int r = (ld.x + lane) * kPgGranule + warp * kPageRows;
-                    pages = -1;
-                    if (ld.x + lane < ld.hi && r < ld.s.hi) {
-                        pages = a.c.table[(long long)ld.b * a.c.width + r / a.c.page_size];
-                        if ((pages < 0 || pages >= a.c.num_pages) && r + kPageRows > ld.s.lo) {
-                            atomicOr(a.flag, kFlagBounds);
-                            pages = -1;
+                    const bool head = ld.x == ld.s.first();
+                    if (head && ld.b == head_b) {
+                        pages = head_pages;
+                    } else {
+                        const int r = (ld.x + lane) * kPgGranule + warp * kPageRows;
+                        pages = -1;
+                        if (ld.x + lane < ld.hi && r < ld.s.hi) {
+                            pages = a.c.table[(long long)ld.b * a.c.width + r / a.c.page_size];
+                            if ((pages < 0 || pages >= a.c.num_pages) && r + kPageRows > ld.s.lo) {
+                                atomicOr(a.flag, kFlagBounds);
+                                pages = -1;
+                            }
                         }
+                        if (head) head_pages = pages, head_b = ld.b;
                     }
-                    fresh = false;
                 }
                 const int page = __shfl_sync(0xffffffffu, pages, ld.x - pg_x);
                 ok = ok && page >= 0;
@@ -392,9 +411,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                 if (ok) pending |= 1u << slot;
             } else {
                 // lane i < 16 finds entry i's row; a missing or bad one is filled with zeros and masked
+                if (fresh) next_e = entry(ld.x);
                 long long off = -1;
                 if (ok && lane < kPageRows && r0 + lane < ld.s.hi) {
-                    const int e = a.idx[((long long)ld.b * Hkv + ld.h) * a.k_max + r0 + lane];
+                    const int e = next_e;
                     const int len = min(max(a.lens[ld.b], 0), a.c.rows_cap());
                     if (e >= len) {
                         atomicOr(a.flag, kFlagBounds);
@@ -407,6 +427,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                                   (long long)(e - pg * a.c.page_size) * a.c.row_stride;
                     }
                 }
+                if (ld.x + 1 < ld.hi) next_e = entry(ld.x + 1);  // on its way while this tile is requested
                 const unsigned valid = __ballot_sync(0xffffffffu, off >= 0);
                 ok = valid != 0;
                 if (ok) {
@@ -433,7 +454,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         auto issue_next = [&](int slot) {
             if (issued < total_g && !dead) {
                 issue(slot);
-                if (++issued < total_g && advance(ld)) fresh = true;
+                fresh = ++issued < total_g && advance(ld);
+                if (fresh) prefetch_q();
             } else if (GATHER) {
                 cp_async_commit();
             }
