@@ -10,7 +10,8 @@
 // A row is read once for g <= 16 query heads (at most 16 flop a byte), so HBM
 // bounds it, and two things decide how near it comes: every SM streaming until
 // the end, and enough bytes in flight.
-//  - Even work whatever the lengths: the granules (64 rows) of all units are
+//  - Even work whatever the lengths: the granules (64 rows) of all units, and one
+//    empty slot after each unit (ending a unit takes about a granule's time), are
 //    laid end to end and each CTA takes the same number of them, so a CTA may end
 //    in the middle of one unit and begin in the middle of another.  The lengths
 //    are on the device only; each warp adds them up itself.  A unit that lies in
@@ -86,11 +87,13 @@ struct Shares {
     }
 };
 
-// Where a sequence's rows begin and end for this pass, in granules of 64 rows.
+// Where a sequence's rows begin and end for this pass, in granules of 64 rows; a unit's
+// slots are its granules and an empty one.
 struct Span {
     int lo, hi;  // rows [lo, hi) (selected rows: entries of the list)
     __device__ __forceinline__ int first() const { return lo / kPgGranule; }
     __device__ __forceinline__ int granules() const { return hi > lo ? (hi + kPgGranule - 1) / kPgGranule - first() : 0; }
+    __device__ __forceinline__ int slots() const { return hi > lo ? granules() + 1 : 0; }
 };
 
 struct PgArgs {
@@ -241,6 +244,7 @@ __device__ __forceinline__ uint32_t movt(uint32_t x) {
 // sequence.
 struct Cursor {
     int b, h, x, hi;  // x in [span.first(), hi)
+    int slot;         // the granule's slot
     Span s;
 };
 
@@ -264,7 +268,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 
     griddep_launch();  // the joining kernel may take its place (it waits for this one's end)
 
-    // ---- the CTA's share: granules [g0, g1) of all units' laid end to end.  Every
+    // ---- the CTA's share: slots [g0, g1) of all units' laid end to end.  Every
     // warp adds up the lengths, four sequences a lane at a time (up to 128
     // sequences: all at once, and the second pass finds them in registers)
     const int B = a.c.B, Hkv = a.c.Hkv;
@@ -273,16 +277,16 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const int b = b0 + lane * 4 + k;
-            cnt[k] = b < B ? span_of<GATHER>(a, b, report).granules() * Hkv : 0;
+            cnt[k] = b < B ? span_of<GATHER>(a, b, report).slots() * Hkv : 0;
         }
         return cnt[0] + cnt[1] + cnt[2] + cnt[3];
     };
     for (int b0 = 0; b0 < B; b0 += 128) total += __reduce_add_sync(0xffffffffu, counts(b0, cta == 0 && warp == 0));
     // CTAs with work.  Few units are not spread over more CTAs than it takes to read
     // them: joining a unit's pieces costs a round trip for each kPgPieces of them.
-    const Shares share(total, (int)min((long long)min((int)gridDim.x, total), max((long long)B * Hkv * kPgPieces, (long long)total / kPgLong)));
+    const Shares share(total, (int)min((long long)min((int)gridDim.x, total), max((long long)B * Hkv * (kPgPieces + 1), (long long)total / kPgLong)));
     const int g0 = cta < share.nc ? share.start(cta) : 0, g1 = cta < share.nc ? share.start(cta + 1) : 0;
-    int first_b = 0, first_base = 0;  // the sequence that holds granule g0, and its first granule
+    int first_b = 0, first_base = 0;  // the sequence that holds slot g0, and its first slot
     for (int b0 = 0, run = 0; b0 < B && g0 < g1; b0 += 128) {
         const int sum = B > 128 ? counts(b0, false) : cnt[0] + cnt[1] + cnt[2] + cnt[3];
         int at = sum;
@@ -314,8 +318,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             c.x = c.s.first();
             c.hi = c.x + c.s.granules();
         };
-        auto advance = [&](Cursor& c) {  // to the next granule (the caller knows there is one)
-            if (++c.x < c.hi) return false;
+        auto next_unit = [&](Cursor& c) {
             if (++c.h == Hkv) {
                 c.h = 0;
                 do {
@@ -325,336 +328,356 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             } else {
                 c.x = c.s.first();
             }
+        };
+        auto advance = [&](Cursor& c) {  // to the next granule (the caller knows there is one); true: of another unit
+            ++c.slot;
+            if (++c.x < c.hi) return false;
+            ++c.slot;
+            next_unit(c);
             return true;
+        };
+        auto more = [&](const Cursor& c) {  // whether a granule of this CTA's comes after it
+            return c.slot + (c.x + 1 < c.hi ? 1 : 2) < g1;
         };
         Cursor at;  // of the consumer
         at.b = first_b;
         enter(at);
-        at.h = (g0 - first_base) / at.s.granules();
-        at.x += g0 - first_base - at.h * at.s.granules();
-        Cursor ld = at;  // of the loads
-        const int total_g = g1 - g0;
+        at.h = (g0 - first_base) / at.s.slots();
+        at.x += g0 - first_base - at.h * at.s.slots();
+        at.slot = g0;
+        // (a share that is one empty slot has no granule)
+        const bool none = at.x == at.hi && g1 == g0 + 1;
+        if (at.x == at.hi && !none) {
+            ++at.slot;
+            next_unit(at);
+        }
+        if (!none) {
+            Cursor ld = at;  // of the loads
 
-        // ---- the products' operand of the unit at hand (its loads are issued before its rows')
-        uint32_t qf[NT][8][2];
-        auto load_q = [&] {
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const int head = t * 8 + (lane >> 2);
-                const uint16_t* qp = a.Q + ((long long)at.b * a.Hq + at.h * a.G + head) * kD + (lane & 3) * 2;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    qf[t][k][0] = head < a.G ? *reinterpret_cast<const uint32_t*>(qp + k * 16) : 0u;
-                    qf[t][k][1] = head < a.G ? *reinterpret_cast<const uint32_t*>(qp + k * 16 + 8) : 0u;
-                }
-            }
-        };
-        load_q();
-
-        // ---- the loads.  Every row: lane i keeps the page of this warp's tile of
-        // granule pg_x + i; the sequence's first 32 are kept apart, since each of its
-        // heads begins with them.  A tile that is not there (no row of the sequence in
-        // it, or a bad page) is not loaded; `there` says so per stage.
-        int pages = -1, pg_b = -1, pg_x = 0, head_pages = -1, head_b = -1;
-        unsigned there = 0, pending = 0, phase = 0;  // bits of the stages: holds a tile; on its way; barrier's phase
-        bool dead = false;                           // a wait gave up: this warp loads and adds no more
-        uint64_t pol = evict_first_policy();
-        bool fresh = true;  // (a list) the loads have come to another unit
-        int next_e = -1;    // lane i < 16: entry i of the next tile
-        auto entry = [&](int x) {
-            const int i = x * kPgGranule + warp * kPageRows + lane;
-            return lane < kPageRows && i < ld.s.hi ? a.idx[((long long)ld.b * Hkv + ld.h) * a.k_max + i] : -1;
-        };
-        auto prefetch_q = [&] {  // the unit's queries, G rows of 256 B
-            const int line = lane & 31;
-            if (line < 2 * a.G)
-                prefetch_l1(a.Q + ((long long)ld.b * a.Hq + ld.h * a.G + (line >> 1)) * kD + (line & 1) * 64);
-        };
-        auto issue = [&](int slot) {
-            const int r0 = ld.x * kPgGranule + warp * kPageRows;  // the tile's first row (or list entry)
-            bool ok = r0 < ld.s.hi && r0 + kPageRows > ld.s.lo;
-            if constexpr (!GATHER) {
-                if (ld.b != pg_b || ld.x < pg_x || ld.x >= pg_x + 32) {
-                    pg_b = ld.b;
-                    pg_x = ld.x;
-                    const bool head = ld.x == ld.s.first();
-                    if (head && ld.b == head_b) {
-                        pages = head_pages;
-                    } else {
-                        const int r = (ld.x + lane) * kPgGranule + warp * kPageRows;
-                        pages = -1;
-                        if (ld.x + lane < ld.hi && r < ld.s.hi) {
-                            pages = a.c.table[(long long)ld.b * a.c.width + r / a.c.page_size];
-                            if ((pages < 0 || pages >= a.c.num_pages) && r + kPageRows > ld.s.lo) {
-                                atomicOr(a.flag, kFlagBounds);
-                                pages = -1;
-                            }
-                        }
-                        if (head) head_pages = pages, head_b = ld.b;
-                    }
-                }
-                const int page = __shfl_sync(0xffffffffu, pages, ld.x - pg_x);
-                ok = ok && page >= 0;
-#ifdef TSA_DEBUG_KNOBS
-                if (ok && lane == 0 && !(cta == 0 && warp == 0 && ld.x == g_debug_paged_skip)) {
-#else
-                if (ok && lane == 0) {
-#endif
-                    const unsigned bar = su32(&s_full[warp * Cfg::kStages + slot]), dst = ring + slot * kPgStage;
-                    const int r = r0 % a.c.page_size;
-                    mbar_arrive_tx(bar, kPgStage);
-                    tma_4d(dst, &kmap, 0, r, ld.h, page, bar, pol);
-                    tma_4d(dst + kPgHalf, &kmap, 64, r, ld.h, page, bar, pol);
-                    tma_4d(dst + 2 * kPgHalf, &vmap, 0, r, ld.h, page, bar, pol);
-                    tma_4d(dst + 3 * kPgHalf, &vmap, 64, r, ld.h, page, bar, pol);
-                }
-                if (ok) pending |= 1u << slot;
-            } else {
-                // lane i < 16 finds entry i's row; a missing or bad one is filled with zeros and masked
-                if (fresh) next_e = entry(ld.x);
-                long long off = -1;
-                if (ok && lane < kPageRows && r0 + lane < ld.s.hi) {
-                    const int e = next_e;
-                    const int len = min(max(a.lens[ld.b], 0), a.c.rows_cap());
-                    if (e >= len) {
-                        atomicOr(a.flag, kFlagBounds);
-                    } else if (e >= 0) {
-                        const int pg = e / a.c.page_size, page = a.c.table[(long long)ld.b * a.c.width + pg];
-                        if (page < 0 || page >= a.c.num_pages)
-                            atomicOr(a.flag, kFlagBounds);
-                        else
-                            off = page * a.c.page_stride + ld.h * a.c.head_stride +
-                                  (long long)(e - pg * a.c.page_size) * a.c.row_stride;
-                    }
-                }
-                if (ld.x + 1 < ld.hi) next_e = entry(ld.x + 1);  // on its way while this tile is requested
-                const unsigned valid = __ballot_sync(0xffffffffu, off >= 0);
-                ok = valid != 0;
-                if (ok) {
-                    const unsigned dst = ring + slot * kPgStage;
-                    const int ch = lane & 15;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int r = (lane >> 4) + 2 * j;
-                        const long long o = __shfl_sync(0xffffffffu, off, r);
-                        const unsigned d = dst + (ch >> 3) * kPgHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
-                        const int n = o >= 0 ? 16 : 0;
-                        const long long e = (o >= 0 ? o : 0) + ch * 8;
-                        cp_async16(d, static_cast<const uint16_t*>(a.c.K) + e, n);
-                        cp_async16(d + 2 * kPgHalf, static_cast<const uint16_t*>(a.c.V) + e, n);
-                    }
-                    // the rows' mask, for the consumer of this stage
-                    if (lane == 0) s_full[warp * Cfg::kStages + slot] = valid;
-                }
-                cp_async_commit();
-            }
-            there = (there & ~(1u << slot)) | ((ok ? 1u : 0u) << slot);
-        };
-        int issued = 0;
-        auto issue_next = [&](int slot) {
-            if (issued < total_g && !dead) {
-                issue(slot);
-                fresh = ++issued < total_g && advance(ld);
-                if (fresh) prefetch_q();
-            } else if (GATHER) {
-                cp_async_commit();
-            }
-        };
-        __syncwarp();
-        for (int i = 0; i < Cfg::kStages; ++i) issue_next(i);
-
-        // ---- the products
-        float acc[NT][8][4], m[NT][2], l[NT][2];
-        bool open = false;  // a unit is being summed
-        int seg0 = 0;       // its first granule here
-        for (int i = 0, slot = 0; i < total_g; ++i, slot = slot + 1 == Cfg::kStages ? 0 : slot + 1) {
-            if (!open) {
-                open = true;
-                seg0 = at.x;
-                if (i > 0) load_q();
+            // ---- the products' operand of the unit at hand (its loads are issued before its rows')
+            uint32_t qf[NT][8][2];
+            auto load_q = [&] {
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
+                    const int head = t * 8 + (lane >> 2);
+                    const uint16_t* qp = a.Q + ((long long)at.b * a.Hq + at.h * a.G + head) * kD + (lane & 3) * 2;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) acc[t][k][0] = acc[t][k][1] = acc[t][k][2] = acc[t][k][3] = 0.f;
-                    m[t][0] = m[t][1] = kNegInf;
-                    l[t][0] = l[t][1] = 0.f;
+                    for (int k = 0; k < 8; ++k) {
+                        qf[t][k][0] = head < a.G ? *reinterpret_cast<const uint32_t*>(qp + k * 16) : 0u;
+                        qf[t][k][1] = head < a.G ? *reinterpret_cast<const uint32_t*>(qp + k * 16 + 8) : 0u;
+                    }
                 }
-            }
-            if constexpr (GATHER) {
-                cp_async_wait<Cfg::kStages - 1>();
-                __syncwarp();
-            }
-            bool here = !dead && (there >> slot & 1u);
-            if (!GATHER && here) {
-                dead = !__all_sync(0xffffffffu, mbar_wait(su32(&s_full[warp * Cfg::kStages + slot]), phase >> slot & 1u, a.flag));
-                here = !dead;
-            }
-            if (here) {
-                const unsigned st = ring + slot * kPgStage;
-                unsigned valid;  // a bit per row of the tile
-                if constexpr (GATHER) {
-                    valid = (unsigned)s_full[warp * Cfg::kStages + slot];
+            };
+            load_q();
+
+            // ---- the loads.  Every row: lane i keeps the page of this warp's tile of
+            // granule pg_x + i; the sequence's first 32 are kept apart, since each of its
+            // heads begins with them.  A tile that is not there (no row of the sequence in
+            // it, or a bad page) is not loaded; `there` says so per stage.
+            int pages = -1, pg_b = -1, pg_x = 0, head_pages = -1, head_b = -1;
+            unsigned there = 0, pending = 0, phase = 0;  // bits of the stages: holds a tile; on its way; barrier's phase
+            bool dead = false;                           // a wait gave up: this warp loads and adds no more
+            uint64_t pol = evict_first_policy();
+            bool fresh = true;  // (a list) the loads have come to another unit
+            int next_e = -1;    // lane i < 16: entry i of the next tile
+            auto entry = [&](int x) {
+                const int i = x * kPgGranule + warp * kPageRows + lane;
+                return lane < kPageRows && i < ld.s.hi ? a.idx[((long long)ld.b * Hkv + ld.h) * a.k_max + i] : -1;
+            };
+            auto prefetch_q = [&] {  // the unit's queries, G rows of 256 B
+                const int line = lane & 31;
+                if (line < 2 * a.G)
+                    prefetch_l1(a.Q + ((long long)ld.b * a.Hq + ld.h * a.G + (line >> 1)) * kD + (line & 1) * 64);
+            };
+            auto issue = [&](int slot) {
+                const int r0 = ld.x * kPgGranule + warp * kPageRows;  // the tile's first row (or list entry)
+                bool ok = r0 < ld.s.hi && r0 + kPageRows > ld.s.lo;
+                if constexpr (!GATHER) {
+                    if (ld.b != pg_b || ld.x < pg_x || ld.x >= pg_x + 32) {
+                        pg_b = ld.b;
+                        pg_x = ld.x;
+                        const bool head = ld.x == ld.s.first();
+                        if (head && ld.b == head_b) {
+                            pages = head_pages;
+                        } else {
+                            const int r = (ld.x + lane) * kPgGranule + warp * kPageRows;
+                            pages = -1;
+                            if (ld.x + lane < ld.hi && r < ld.s.hi) {
+                                pages = a.c.table[(long long)ld.b * a.c.width + r / a.c.page_size];
+                                if ((pages < 0 || pages >= a.c.num_pages) && r + kPageRows > ld.s.lo) {
+                                    atomicOr(a.flag, kFlagBounds);
+                                    pages = -1;
+                                }
+                            }
+                            if (head) head_pages = pages, head_b = ld.b;
+                        }
+                    }
+                    const int page = __shfl_sync(0xffffffffu, pages, ld.x - pg_x);
+                    ok = ok && page >= 0;
+#ifdef TSA_DEBUG_KNOBS
+                    if (ok && lane == 0 && !(cta == 0 && warp == 0 && ld.x == g_debug_paged_skip)) {
+#else
+                    if (ok && lane == 0) {
+#endif
+                        const unsigned bar = su32(&s_full[warp * Cfg::kStages + slot]), dst = ring + slot * kPgStage;
+                        const int r = r0 % a.c.page_size;
+                        mbar_arrive_tx(bar, kPgStage);
+                        tma_4d(dst, &kmap, 0, r, ld.h, page, bar, pol);
+                        tma_4d(dst + kPgHalf, &kmap, 64, r, ld.h, page, bar, pol);
+                        tma_4d(dst + 2 * kPgHalf, &vmap, 0, r, ld.h, page, bar, pol);
+                        tma_4d(dst + 3 * kPgHalf, &vmap, 64, r, ld.h, page, bar, pol);
+                    }
+                    if (ok) pending |= 1u << slot;
                 } else {
-                    phase ^= 1u << slot;
-                    pending &= ~(1u << slot);
-                    const int r0 = at.x * kPgGranule + warp * kPageRows;
-                    valid = 0xffffu;
-                    if (r0 + kPageRows > at.s.hi) valid &= 0xffffu >> (r0 + kPageRows - at.s.hi);
-                    if (r0 < at.s.lo) valid &= 0xffffu << (at.s.lo - r0);
-                    valid &= 0xffffu;
-                    if (valid != 0xffffu) {
-                        unsigned char* vp = ringp + slot * kPgStage + 2 * kPgHalf;
+                    // lane i < 16 finds entry i's row; a missing or bad one is filled with zeros and masked
+                    if (fresh) next_e = entry(ld.x);
+                    long long off = -1;
+                    if (ok && lane < kPageRows && r0 + lane < ld.s.hi) {
+                        const int e = next_e;
+                        const int len = min(max(a.lens[ld.b], 0), a.c.rows_cap());
+                        if (e >= len) {
+                            atomicOr(a.flag, kFlagBounds);
+                        } else if (e >= 0) {
+                            const int pg = e / a.c.page_size, page = a.c.table[(long long)ld.b * a.c.width + pg];
+                            if (page < 0 || page >= a.c.num_pages)
+                                atomicOr(a.flag, kFlagBounds);
+                            else
+                                off = page * a.c.page_stride + ld.h * a.c.head_stride +
+                                      (long long)(e - pg * a.c.page_size) * a.c.row_stride;
+                        }
+                    }
+                    if (ld.x + 1 < ld.hi) next_e = entry(ld.x + 1);  // on its way while this tile is requested
+                    const unsigned valid = __ballot_sync(0xffffffffu, off >= 0);
+                    ok = valid != 0;
+                    if (ok) {
+                        const unsigned dst = ring + slot * kPgStage;
+                        const int ch = lane & 15;
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             const int r = (lane >> 4) + 2 * j;
-                            if (!(valid >> r & 1u))
-                                *reinterpret_cast<uint4*>(vp + (lane >> 3 & 1) * kPgHalf + r * 128 + (lane & 7) * 16) =
-                                    make_uint4(0, 0, 0, 0);
+                            const long long o = __shfl_sync(0xffffffffu, off, r);
+                            const unsigned d = dst + (ch >> 3) * kPgHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+                            const int n = o >= 0 ? 16 : 0;
+                            const long long e = (o >= 0 ? o : 0) + ch * 8;
+                            cp_async16(d, static_cast<const uint16_t*>(a.c.K) + e, n);
+                            cp_async16(d + 2 * kPgHalf, static_cast<const uint16_t*>(a.c.V) + e, n);
                         }
-                        fence_proxy_async();  // before the next copy into this stage
-                        __syncwarp();
+                        // the rows' mask, for the consumer of this stage
+                        if (lane == 0) s_full[warp * Cfg::kStages + slot] = valid;
                     }
+                    cp_async_commit();
                 }
-                float s[NT][4], s2[NT][4];  // two chains of products
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) s[t][j] = s2[t][j] = 0.f;
-                const int fr = lane & 15, fc = lane >> 4;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    uint32_t kf[4];
-                    ldsm4(kf, st + (k >> 2) * kPgHalf + fr * 128 + ((((k & 3) * 2 + fc) ^ (fr & 7)) << 4));
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) E::mma(k & 1 ? s2[t] : s[t], kf, qf[t][k][0], qf[t][k][1]);
+                there = (there & ~(1u << slot)) | ((ok ? 1u : 0u) << slot);
+            };
+            bool rest = true;  // granules of this CTA's not yet requested
+            auto issue_next = [&](int slot) {
+                if (rest && !dead) {
+                    issue(slot);
+                    rest = more(ld);
+                    fresh = rest && advance(ld);
+                    if (fresh) prefetch_q();
+                } else if (GATHER) {
+                    cp_async_commit();
                 }
-                const int row = lane >> 2;
-                const bool v0 = valid >> row & 1u, v1 = valid >> (row + 8) & 1u;
-                bool up = false;
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) s[t][j] = (j < 2 ? v0 : v1) ? (s[t][j] + s2[t][j]) * a.scale_log2 : kNegInf;
-                    up |= fmaxf(s[t][0], s[t][2]) > m[t][0] || fmaxf(s[t][1], s[t][3]) > m[t][1];
-                }
-                if (__any_sync(0xffffffffu, up)) {  // a larger maximum: rescale what there is
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            float x = fmaxf(s[t][j], s[t][j + 2]);
-                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                            x = fmaxf(x, m[t][j]);
-                            const float f = x == kNegInf ? 1.f : exp2f(m[t][j] - x);
-                            m[t][j] = x;
-                            l[t][j] *= f;
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) acc[t][k][j] *= f, acc[t][k][j + 2] *= f;
-                        }
-                    }
-                }
-                uint32_t ph[NT][2], pl[NT][2];
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    // (no row so far: the scores are -inf and the weights 0)
-                    const float ms[2] = {m[t][0] == kNegInf ? 0.f : m[t][0], m[t][1] == kNegInf ? 0.f : m[t][1]};
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        // j = 0: rows 0-7, j = 1: rows 8-15; two heads each
-                        const float p0 = exp2f(s[t][2 * j] - ms[0]), p1 = exp2f(s[t][2 * j + 1] - ms[1]);
-                        l[t][0] += p0;
-                        l[t][1] += p1;
-                        const uint32_t hi = E::pack(p0, p1);
-                        ph[t][j] = movt(hi);
-                        pl[t][j] = movt(E::pack(p0 - E::lo(hi), p1 - E::hi(hi)));
-                    }
-                }
-                // V^T fragments: rows of the stage are tokens, 16 dims an m-tile
-                const int vr = (lane & 7) + (lane >> 4) * 8, vc = lane >> 3 & 1;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    uint32_t vf[4];
-                    ldsm4t(vf, st + (2 + (k >> 2)) * kPgHalf + vr * 128 + ((((k & 3) * 2 + vc) ^ (vr & 7)) << 4));
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        E::mma(acc[t][k], vf, ph[t][0], ph[t][1]);
-                        E::mma(acc[t][k], vf, pl[t][0], pl[t][1]);
-                    }
-                }
-            }
+            };
             __syncwarp();
-            issue_next(slot);
+            for (int i = 0; i < Cfg::kStages; ++i) issue_next(i);
 
-            // ---- the end of the unit here
-            const Cursor cur = at;
-            const bool last = i + 1 == total_g;
-            if (!last && !advance(at)) continue;
-            open = false;
+            // ---- the products
+            float acc[NT][8][4], m[NT][2], l[NT][2];
+            bool open = false;  // a unit is being summed
+            int seg0 = 0;       // its first granule here
+            bool last = false, loaded_q = true;
+            for (int slot = 0; !last; slot = slot + 1 == Cfg::kStages ? 0 : slot + 1) {
+                if (!open) {
+                    open = true;
+                    seg0 = at.x;
+                    if (!loaded_q) load_q();
+                    loaded_q = false;
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
+                    for (int t = 0; t < NT; ++t) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float x = l[t][j];
-                    x += __shfl_xor_sync(0xffffffffu, x, 4);
-                    x += __shfl_xor_sync(0xffffffffu, x, 8);
-                    x += __shfl_xor_sync(0xffffffffu, x, 16);
-                    const int head = t * 8 + (lane & 3) * 2 + j;
-                    float* w = merge + (warp * Cfg::kHeads + head) * kPartFloats;
-                    if (lane < 4) {
-                        w[kD] = m[t][j];
-                        w[kD + 1] = x;
+                        for (int k = 0; k < 8; ++k) acc[t][k][0] = acc[t][k][1] = acc[t][k][2] = acc[t][k][3] = 0.f;
+                        m[t][0] = m[t][1] = kNegInf;
+                        l[t][0] = l[t][1] = 0.f;
                     }
+                }
+                if constexpr (GATHER) {
+                    cp_async_wait<Cfg::kStages - 1>();
+                    __syncwarp();
+                }
+                bool here = !dead && (there >> slot & 1u);
+                if (!GATHER && here) {
+                    dead = !__all_sync(0xffffffffu, mbar_wait(su32(&s_full[warp * Cfg::kStages + slot]), phase >> slot & 1u, a.flag));
+                    here = !dead;
+                }
+                if (here) {
+                    const unsigned st = ring + slot * kPgStage;
+                    unsigned valid;  // a bit per row of the tile
+                    if constexpr (GATHER) {
+                        valid = (unsigned)s_full[warp * Cfg::kStages + slot];
+                    } else {
+                        phase ^= 1u << slot;
+                        pending &= ~(1u << slot);
+                        const int r0 = at.x * kPgGranule + warp * kPageRows;
+                        valid = 0xffffu;
+                        if (r0 + kPageRows > at.s.hi) valid &= 0xffffu >> (r0 + kPageRows - at.s.hi);
+                        if (r0 < at.s.lo) valid &= 0xffffu << (at.s.lo - r0);
+                        valid &= 0xffffu;
+                        if (valid != 0xffffu) {
+                            unsigned char* vp = ringp + slot * kPgStage + 2 * kPgHalf;
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const int r = (lane >> 4) + 2 * j;
+                                if (!(valid >> r & 1u))
+                                    *reinterpret_cast<uint4*>(vp + (lane >> 3 & 1) * kPgHalf + r * 128 + (lane & 7) * 16) =
+                                        make_uint4(0, 0, 0, 0);
+                            }
+                            fence_proxy_async();  // before the next copy into this stage
+                            __syncwarp();
+                        }
+                    }
+                    float s[NT][4], s2[NT][4];  // two chains of products
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) s[t][j] = s2[t][j] = 0.f;
+                    const int fr = lane & 15, fc = lane >> 4;
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        w[k * 16 + (lane >> 2)] = acc[t][k][j];
-                        w[k * 16 + (lane >> 2) + 8] = acc[t][k][j + 2];
+                        uint32_t kf[4];
+                        ldsm4(kf, st + (k >> 2) * kPgHalf + fr * 128 + ((((k & 3) * 2 + fc) ^ (fr & 7)) << 4));
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) E::mma(k & 1 ? s2[t] : s[t], kf, qf[t][k][0], qf[t][k][1]);
+                    }
+                    const int row = lane >> 2;
+                    const bool v0 = valid >> row & 1u, v1 = valid >> (row + 8) & 1u;
+                    bool up = false;
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) s[t][j] = (j < 2 ? v0 : v1) ? (s[t][j] + s2[t][j]) * a.scale_log2 : kNegInf;
+                        up |= fmaxf(s[t][0], s[t][2]) > m[t][0] || fmaxf(s[t][1], s[t][3]) > m[t][1];
+                    }
+                    if (__any_sync(0xffffffffu, up)) {  // a larger maximum: rescale what there is
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                float x = fmaxf(s[t][j], s[t][j + 2]);
+                                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                                x = fmaxf(x, m[t][j]);
+                                const float f = x == kNegInf ? 1.f : exp2f(m[t][j] - x);
+                                m[t][j] = x;
+                                l[t][j] *= f;
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) acc[t][k][j] *= f, acc[t][k][j + 2] *= f;
+                            }
+                        }
+                    }
+                    uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        // (no row so far: the scores are -inf and the weights 0)
+                        const float ms[2] = {m[t][0] == kNegInf ? 0.f : m[t][0], m[t][1] == kNegInf ? 0.f : m[t][1]};
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            // j = 0: rows 0-7, j = 1: rows 8-15; two heads each
+                            const float p0 = exp2f(s[t][2 * j] - ms[0]), p1 = exp2f(s[t][2 * j + 1] - ms[1]);
+                            l[t][0] += p0;
+                            l[t][1] += p1;
+                            const uint32_t hi = E::pack(p0, p1);
+                            ph[t][j] = movt(hi);
+                            pl[t][j] = movt(E::pack(p0 - E::lo(hi), p1 - E::hi(hi)));
+                        }
+                    }
+                    // V^T fragments: rows of the stage are tokens, 16 dims an m-tile
+                    const int vr = (lane & 7) + (lane >> 4) * 8, vc = lane >> 3 & 1;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        uint32_t vf[4];
+                        ldsm4t(vf, st + (2 + (k >> 2)) * kPgHalf + vr * 128 + ((((k & 3) * 2 + vc) ^ (vr & 7)) << 4));
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            E::mma(acc[t][k], vf, ph[t][0], ph[t][1]);
+                            E::mma(acc[t][k], vf, pl[t][0], pl[t][1]);
+                        }
                     }
                 }
-            }
-            __syncthreads();
-            const bool whole = seg0 == cur.s.first() && cur.x + 1 == cur.hi;
-            const int u0 = g0 + i - (cur.x - cur.s.first());  // the unit's first granule, laid end to end
-            // a CTA's pieces: of the unit it begins in, then of the unit it ends in
-            float* piece = a.pieces + (2LL * cta + (u0 > g0 ? 1 : 0)) * a.G * kPartFloats;
-            if (tid == 0 && u0 >= g0) {  // the unit begins here
-                const int c1 = share.cta_of(u0 + cur.s.granules() - 1);
-                a.units[(long long)cur.b * Hkv + cur.h] = make_int2(2 * cta + (u0 > g0 ? 1 : 0), whole ? 0 : c1 - cta + 1);
-            }
-            for (int g = warp; g < a.G; g += kPgWarps) {
-                float M = kNegInf, L = 0.f, f[kPgWarps];
-                const float* w = merge + g * kPartFloats;
-                constexpr int S = Cfg::kHeads * kPartFloats;
+                __syncwarp();
+                issue_next(slot);
+
+                // ---- the end of the unit here
+                const Cursor cur = at;
+                last = !more(at);
+                if (!last && !advance(at)) continue;
+                open = false;
 #pragma unroll
-                for (int k = 0; k < kPgWarps; ++k) M = fmaxf(M, w[k * S + kD]);
+                for (int t = 0; t < NT; ++t) {
 #pragma unroll
-                for (int k = 0; k < kPgWarps; ++k) {
-                    const float mk = w[k * S + kD];
-                    f[k] = mk == kNegInf ? 0.f : exp2f(mk - M);
-                    L += (mk == kNegInf ? w[k * S + kD + 1] * 0.f : f[k] * w[k * S + kD + 1]);
-                }
-                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int j = 0; j < 2; ++j) {
+                        float x = l[t][j];
+                        x += __shfl_xor_sync(0xffffffffu, x, 4);
+                        x += __shfl_xor_sync(0xffffffffu, x, 8);
+                        x += __shfl_xor_sync(0xffffffffu, x, 16);
+                        const int head = t * 8 + (lane & 3) * 2 + j;
+                        float* w = merge + (warp * Cfg::kHeads + head) * kPartFloats;
+                        if (lane < 4) {
+                            w[kD] = m[t][j];
+                            w[kD + 1] = x;
+                        }
 #pragma unroll
-                for (int k = 0; k < kPgWarps; ++k) {
-                    const float4 v = *(reinterpret_cast<const float4*>(w + k * S) + lane);
-                    o.x = fmaf(f[k], v.x, o.x), o.y = fmaf(f[k], v.y, o.y);
-                    o.z = fmaf(f[k], v.z, o.z), o.w = fmaf(f[k], v.w, o.w);
+                        for (int k = 0; k < 8; ++k) {
+                            w[k * 16 + (lane >> 2)] = acc[t][k][j];
+                            w[k * 16 + (lane >> 2) + 8] = acc[t][k][j + 2];
+                        }
+                    }
                 }
-                if (whole) {
-                    put_row<E>(a, (long long)cur.b * a.Hq + cur.h * a.G + g, o, M, L, lane);
-                } else {
-                    float* p = piece + g * kPartFloats;
-                    __stcg(reinterpret_cast<float4*>(p) + lane, o);
-                    if (lane == 0) __stcg(reinterpret_cast<float2*>(p + kD), make_float2(M, L));
+                __syncthreads();
+                const bool whole = seg0 == cur.s.first() && cur.x + 1 == cur.hi;
+                const int u0 = cur.slot - (cur.x - cur.s.first());  // the unit's first slot
+                // a CTA's pieces: of the unit it begins in, then of the unit it ends in
+                float* piece = a.pieces + (2LL * cta + (u0 > g0 ? 1 : 0)) * a.G * kPartFloats;
+                if (tid == 0 && u0 >= g0) {  // the unit begins here
+                    const int c1 = share.cta_of(u0 + cur.s.granules() - 1);
+                    a.units[(long long)cur.b * Hkv + cur.h] = make_int2(2 * cta + (u0 > g0 ? 1 : 0), whole ? 0 : c1 - cta + 1);
                 }
+                for (int g = warp; g < a.G; g += kPgWarps) {
+                    float M = kNegInf, L = 0.f, f[kPgWarps];
+                    const float* w = merge + g * kPartFloats;
+                    constexpr int S = Cfg::kHeads * kPartFloats;
+#pragma unroll
+                    for (int k = 0; k < kPgWarps; ++k) M = fmaxf(M, w[k * S + kD]);
+#pragma unroll
+                    for (int k = 0; k < kPgWarps; ++k) {
+                        const float mk = w[k * S + kD];
+                        f[k] = mk == kNegInf ? 0.f : exp2f(mk - M);
+                        L += (mk == kNegInf ? w[k * S + kD + 1] * 0.f : f[k] * w[k * S + kD + 1]);
+                    }
+                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int k = 0; k < kPgWarps; ++k) {
+                        const float4 v = *(reinterpret_cast<const float4*>(w + k * S) + lane);
+                        o.x = fmaf(f[k], v.x, o.x), o.y = fmaf(f[k], v.y, o.y);
+                        o.z = fmaf(f[k], v.z, o.z), o.w = fmaf(f[k], v.w, o.w);
+                    }
+                    if (whole) {
+                        put_row<E>(a, (long long)cur.b * a.Hq + cur.h * a.G + g, o, M, L, lane);
+                    } else {
+                        float* p = piece + g * kPartFloats;
+                        __stcg(reinterpret_cast<float4*>(p) + lane, o);
+                        if (lane == 0) __stcg(reinterpret_cast<float2*>(p + kD), make_float2(M, L));
+                    }
+                }
+                __syncthreads();  // the merge buffer is free again
             }
-            __syncthreads();  // the merge buffer is free again
+            if (GATHER) cp_async_wait<0>();
+            // (only after a wait gave up) nothing lands after the CTA has gone
+            for (int i = 0; i < Cfg::kStages; ++i)
+                if (pending >> i & 1u) mbar_wait(su32(&s_full[warp * Cfg::kStages + i]), phase >> i & 1u, nullptr);
         }
-        if (GATHER) cp_async_wait<0>();
-        // (only after a wait gave up) nothing lands after the CTA has gone
-        for (int i = 0; i < Cfg::kStages; ++i)
-            if (pending >> i & 1u) mbar_wait(su32(&s_full[warp * Cfg::kStages + i]), phase >> i & 1u, nullptr);
     }
 
     if (a.pre.splits > 0) griddep_wait();  // the prefix's pass is over before this one counts as over
