@@ -198,7 +198,7 @@ tsa_status attn(const tsa_paged_attn_args* a, bool prefix, const char* what, voi
         if (!aligned16(a->Q) || !aligned16(a->O)) return fail(TSA_ERR_INVALID_ARG, "%s: Q and O must be 16-byte aligned", what);
         if (a->O == a->Q) return fail(TSA_ERR_INVALID_ARG, "%s: O must not be Q", what);
     }
-    if ((long long)c.B * c.Hkv * ((c.rows_cap() + 63LL) / 64 + 1) > INT32_MAX)
+    if ((long long)c.B * c.Hkv * ((c.rows_cap() + 63LL) / 64 + 4) > INT32_MAX)
         return fail(TSA_ERR_UNSUPPORTED, "%s: B*Hkv*max_pages*page_size above 2^37 rows", what);
     const Layout L = layout(c, a->Hq, a->prefix_len);
     TSA_TRY(check_ws(a->ws, a->ws_bytes, L.total));

@@ -52,6 +52,7 @@ constexpr int kPgHalf = kPageRows * 128;           // 64 elements of 16 rows: 2 
 constexpr int kPgStage = 4 * kPgHalf;              // K halves, V halves: 8 KB
 constexpr int kPgCtasPerSm = 2;
 constexpr int kPgPieces = 64;  // pieces of a unit that one round of loads joins
+constexpr int kPgEnd = 1;      // empty slots after a unit
 constexpr int kPgLong = 8;     // granules a CTA above which more pieces pay
 constexpr float kNegInf = -INFINITY;
 
@@ -93,7 +94,7 @@ struct Span {
     int lo, hi;  // rows [lo, hi) (selected rows: entries of the list)
     __device__ __forceinline__ int first() const { return lo / kPgGranule; }
     __device__ __forceinline__ int granules() const { return hi > lo ? (hi + kPgGranule - 1) / kPgGranule - first() : 0; }
-    __device__ __forceinline__ int slots() const { return hi > lo ? granules() + 1 : 0; }
+    __device__ __forceinline__ int slots() const { return hi > lo ? granules() + kPgEnd : 0; }
 };
 
 struct PgArgs {
@@ -284,7 +285,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     for (int b0 = 0; b0 < B; b0 += 128) total += __reduce_add_sync(0xffffffffu, counts(b0, cta == 0 && warp == 0));
     // CTAs with work.  Few units are not spread over more CTAs than it takes to read
     // them: joining a unit's pieces costs a round trip for each kPgPieces of them.
-    const Shares share(total, (int)min((long long)min((int)gridDim.x, total), max((long long)B * Hkv * (kPgPieces + 1), (long long)total / kPgLong)));
+    const Shares share(total, (int)min((long long)min((int)gridDim.x, total),
+                                       max((long long)B * Hkv * (kPgPieces + kPgEnd), (long long)total / kPgLong)));
     const int g0 = cta < share.nc ? share.start(cta) : 0, g1 = cta < share.nc ? share.start(cta + 1) : 0;
     int first_b = 0, first_base = 0;  // the sequence that holds slot g0, and its first slot
     for (int b0 = 0, run = 0; b0 < B && g0 < g1; b0 += 128) {
@@ -332,23 +334,24 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         auto advance = [&](Cursor& c) {  // to the next granule (the caller knows there is one); true: of another unit
             ++c.slot;
             if (++c.x < c.hi) return false;
-            ++c.slot;
+            c.slot += kPgEnd;
             next_unit(c);
             return true;
         };
         auto more = [&](const Cursor& c) {  // whether a granule of this CTA's comes after it
-            return c.slot + (c.x + 1 < c.hi ? 1 : 2) < g1;
+            return c.slot + (c.x + 1 < c.hi ? 1 : 1 + kPgEnd) < g1;
         };
         Cursor at;  // of the consumer
         at.b = first_b;
         enter(at);
         at.h = (g0 - first_base) / at.s.slots();
-        at.x += g0 - first_base - at.h * at.s.slots();
+        const int off = g0 - first_base - at.h * at.s.slots(), gap = at.s.slots() - off;
+        at.x += off;
         at.slot = g0;
-        // (a share that is one empty slot has no granule)
-        const bool none = at.x == at.hi && g1 == g0 + 1;
-        if (at.x == at.hi && !none) {
-            ++at.slot;
+        // (a share may begin with empty slots, and be nothing else)
+        const bool empty = gap <= kPgEnd, none = empty && gap >= g1 - g0;
+        if (empty && !none) {
+            at.slot += gap;
             next_unit(at);
         }
         if (!none) {
