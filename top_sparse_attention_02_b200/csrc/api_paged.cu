@@ -148,10 +148,10 @@ tsa_status check_ws(const void* ws, size_t ws_bytes, size_t need) {
     return TSA_OK;
 }
 
-// [flag 256 B][each unit's pieces][the CTAs' pieces][a shared prefix's partials, and
+// [flag 256 B][the CTAs' pieces][a shared prefix's partials, and
 // those of the sequences' own rows]
 struct Layout {
-    size_t units, pieces, parts, total;
+    size_t pieces, parts, total;
 };
 
 // Whether the prefix gets its own pass.  It saves reading the prefix's rows again for
@@ -166,8 +166,6 @@ bool shares(const tsa::Pages& c, int prefix_len) {
 Layout layout(const tsa::Pages& c, int Hq, int prefix_len) {
     Layout L;
     size_t off = kFlagBytes;
-    L.units = off;
-    off += a256((size_t)c.B * c.Hkv * 2 * sizeof(int32_t));
     L.pieces = off;
     off += a256((size_t)2 * tsa::paged_ctas() * (Hq / c.Hkv) * tsa::kPartFloats * sizeof(float));
     L.parts = off;
@@ -214,7 +212,7 @@ tsa_status attn(const tsa_paged_attn_args* a, bool prefix, const char* what, voi
     }
     const cudaError_t e = tsa::launch_paged_attn(c, a->Q, a->Hq, a->seq_lens, a->idx, a->k_per_seq, a->k_max, a->scale,
                                                  a->O, a->lse, reinterpret_cast<float*>(w + L.pieces),
-                                                 reinterpret_cast<int32_t*>(w + L.units), pre, flag, st);
+                                                 pre, flag, st);
     if (e != cudaSuccess) return cuda_fail(e, what);
     return TSA_OK;
 }

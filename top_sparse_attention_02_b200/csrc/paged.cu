@@ -51,6 +51,7 @@ constexpr int kPgGranule = kPgWarps * kPageRows;   // rows
 constexpr int kPgHalf = kPageRows * 128;           // 64 elements of 16 rows: 2 KB
 constexpr int kPgStage = 4 * kPgHalf;              // K halves, V halves: 8 KB
 constexpr int kPgCtasPerSm = 2;
+constexpr int kPgCtas = kPgCtasPerSm * kPagedSms;  // the grid
 constexpr int kPgPieces = 64;  // pieces of a unit that one round of loads joins
 constexpr int kPgEnd = 1;      // empty slots after a unit
 constexpr int kPgLong = 8;     // granules a CTA above which more pieces pay
@@ -73,7 +74,7 @@ struct PgCfg {
     static constexpr int kSmem = kBars + kPgWarps * kStages * 8;
 };
 
-int paged_ctas() { return kPgCtasPerSm * kPagedSms; }
+int paged_ctas() { return kPgCtas; }
 
 // n granules over nc CTAs: the first n % nc take one more
 struct Shares {
@@ -107,7 +108,6 @@ struct PgArgs {
     uint16_t* O;
     float* lse;
     float* pieces;       // [2 * gridDim.x][G][kPartFloats]
-    int2* units;         // [B * Hkv]: a unit's first piece and their number (0: the CTA that holds it wrote its rows)
     PrefixParts pre;
     float* own;          // over a shared prefix: [B][Hq][kPartFloats], where this pass's partials go
     unsigned* flag;
@@ -135,6 +135,22 @@ __device__ __forceinline__ Span span_of(const PgArgs& a, int b, bool report) {
         s.lo = a.pre.prefix_len;
     }
     return s;
+}
+
+// The slots of the sequences b0 + 4 lane .. + 3 (all heads), and the shares of them all.
+template <bool GATHER>
+__device__ __forceinline__ void slots4(const PgArgs& a, int b0, int lane, bool report, int (&cnt)[4]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int b = b0 + lane * 4 + k;
+        cnt[k] = b < a.c.B ? span_of<GATHER>(a, b, report).slots() * a.c.Hkv : 0;
+    }
+}
+// CTAs with work: few units are not spread over more CTAs than it takes to read them
+// (joining a unit's pieces costs a round trip for each kPgPieces of them).
+__device__ __forceinline__ Shares shares_of(const PgArgs& a, int total) {
+    return Shares(total, (int)min((long long)min(kPgCtas, total),
+                                  max((long long)a.c.B * a.c.Hkv * (kPgPieces + kPgEnd), (long long)total / kPgLong)));
 }
 
 // A row's result out of its sums acc (4 of 128 a lane), maximum M and weight L.
@@ -274,23 +290,16 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     // sequences: all at once, and the second pass finds them in registers)
     const int B = a.c.B, Hkv = a.c.Hkv;
     int cnt[4], total = 0;
-    auto counts = [&](int b0, bool report) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int b = b0 + lane * 4 + k;
-            cnt[k] = b < B ? span_of<GATHER>(a, b, report).slots() * Hkv : 0;
-        }
-        return cnt[0] + cnt[1] + cnt[2] + cnt[3];
-    };
-    for (int b0 = 0; b0 < B; b0 += 128) total += __reduce_add_sync(0xffffffffu, counts(b0, cta == 0 && warp == 0));
-    // CTAs with work.  Few units are not spread over more CTAs than it takes to read
-    // them: joining a unit's pieces costs a round trip for each kPgPieces of them.
-    const Shares share(total, (int)min((long long)min((int)gridDim.x, total),
-                                       max((long long)B * Hkv * (kPgPieces + kPgEnd), (long long)total / kPgLong)));
+    for (int b0 = 0; b0 < B; b0 += 128) {
+        slots4<GATHER>(a, b0, lane, cta == 0 && warp == 0, cnt);
+        total += __reduce_add_sync(0xffffffffu, cnt[0] + cnt[1] + cnt[2] + cnt[3]);
+    }
+    const Shares share = shares_of(a, total);
     const int g0 = cta < share.nc ? share.start(cta) : 0, g1 = cta < share.nc ? share.start(cta + 1) : 0;
     int first_b = 0, first_base = 0;  // the sequence that holds slot g0, and its first slot
     for (int b0 = 0, run = 0; b0 < B && g0 < g1; b0 += 128) {
-        const int sum = B > 128 ? counts(b0, false) : cnt[0] + cnt[1] + cnt[2] + cnt[3];
+        if (B > 128) slots4<GATHER>(a, b0, lane, false, cnt);
+        const int sum = cnt[0] + cnt[1] + cnt[2] + cnt[3];
         int at = sum;
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
@@ -643,10 +652,6 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                 const int u0 = cur.slot - (cur.x - cur.s.first());  // the unit's first slot
                 // a CTA's pieces: of the unit it begins in, then of the unit it ends in
                 float* piece = a.pieces + (2LL * cta + (u0 > g0 ? 1 : 0)) * a.G * kPartFloats;
-                if (tid == 0 && u0 >= g0) {  // the unit begins here
-                    const int c1 = share.cta_of(u0 + cur.s.granules() - 1);
-                    a.units[(long long)cur.b * Hkv + cur.h] = make_int2(2 * cta + (u0 > g0 ? 1 : 0), whole ? 0 : c1 - cta + 1);
-                }
                 for (int g = warp; g < a.G; g += kPgWarps) {
                     float M = kNegInf, L = 0.f, f[kPgWarps];
                     const float* w = merge + g * kPartFloats;
@@ -692,32 +697,51 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 // row gets zeros.  W warps a row, each with a part of the partials, whose loads are
 // all on their way at once.
 constexpr int kJoinWarps = 8;
-constexpr int kMaxPieces = kPgCtasPerSm * kPagedSms;
 template <class E, int W, bool GATHER>
 __global__ void __launch_bounds__(32 * kJoinWarps)
 paged_join_kernel(const PgArgs a, int rows) {
-    __shared__ float wts[kJoinWarps][kMaxPrefixSplits + kMaxPieces];
+    __shared__ float wts[kJoinWarps][kMaxPrefixSplits + kPgCtas];
     __shared__ float4 sums[kJoinWarps][32];
-    griddep_wait();
-    griddep_launch();
+    __shared__ int2 red[kJoinWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = warp % W;
     const int row = blockIdx.x * (kJoinWarps / W) + warp / W;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float M = kNegInf, L = 0.f;
     bool mine = row < rows;
+    // Where the row's pieces lie follows from the lengths, which the kernels before this
+    // one only read: found before the wait on them.
+    const int b = min(row, rows - 1) / a.Hq, r = min(row, rows - 1) - b * a.Hq, h = r / a.G, g = r - h * a.G;
+    const int b_lo = blockIdx.x * (kJoinWarps / W) / a.Hq;  // (the CTA adds up the lengths once)
+    int total = 0, u0 = 0;
+    for (int i = threadIdx.x; i < a.c.B; i += 32 * kJoinWarps) {
+        const int v = span_of<GATHER>(a, i, false).slots() * a.c.Hkv;
+        total += v;
+        if (i < b_lo) u0 += v;
+    }
+    total = __reduce_add_sync(0xffffffffu, total);
+    u0 = __reduce_add_sync(0xffffffffu, u0);
+    if (lane == 0) red[warp] = make_int2(total, u0);
+    __syncthreads();
+    total = u0 = 0;
+#pragma unroll
+    for (int i = 0; i < kJoinWarps; ++i) total += red[i].x, u0 += red[i].y;
+    for (int i = b_lo; i < b; ++i) u0 += span_of<GATHER>(a, i, false).slots() * a.c.Hkv;
+    const Span s = span_of<GATHER>(a, b, false);
+    const Shares share = shares_of(a, total);
+    u0 += h * s.slots();  // the unit's first slot
+    const bool some = s.granules() > 0;
+    const int c0 = some ? share.cta_of(u0) : 0, c1 = some ? share.cta_of(u0 + s.granules() - 1) : 0;
+    const int first = 2 * c0 + (u0 > share.start(c0) ? 1 : 0);  // its first piece; the others are their CTAs' first
+    griddep_wait();
+    griddep_launch();
     if (mine) {
-        const int b = row / a.Hq, r = row - b * a.Hq, h = r / a.G, g = r - h * a.G;
-        const int2 unit = a.units[(long long)b * a.c.Hkv + h];  // (of no meaning without rows of its own)
-        const Span s = span_of<GATHER>(a, b, false);
         const int n0 = s.lo > 0 ? a.pre.splits : 0;
-        const bool some = s.granules() > 0, own = some && unit.y == 0;
-        const int n = n0 + (some ? max(unit.y, 1) : 0);
+        const bool own = some && c0 == c1;
+        const int n = n0 + (some ? c1 - c0 + 1 : 0);
         auto part = [&](int i) -> const float* {
             if (i < n0) return a.pre.parts + ((long long)i * rows + row) * kPartFloats;
             if (own) return a.own + (long long)row * kPartFloats;
-            // the first piece is either of its CTA's, the others are their CTAs' first
-            const int slot = i == n0 ? unit.x : (unit.x / 2 + i - n0) * 2;
-            return a.pieces + ((long long)slot * a.G + g) * kPartFloats;
+            return a.pieces + ((long long)(i == n0 ? first : (c0 + i - n0) * 2) * a.G + g) * kPartFloats;
         };
         mine = !(own && !a.own);
         if (mine) o = join_sums(n, w, W, part, wts[warp], lane, [&] { join_weights(n, part, wts[warp], lane, &M, &L); });
@@ -786,7 +810,7 @@ static cudaError_t paged_pick(int grid, const CUtensorMap& km, const CUtensorMap
 
 cudaError_t launch_paged_attn(const Pages& c, const void* Q, int Hq, const int32_t* lens, const int32_t* idx,
                               const int32_t* kreq, int k_max, float scale, void* O, float* lse, float* pieces,
-                              int32_t* units, const PrefixParts& pre, unsigned* flag, cudaStream_t st) {
+                              const PrefixParts& pre, unsigned* flag, cudaStream_t st) {
     if (c.B == 0) return cudaSuccess;
     PgArgs a;
     a.c = c;
@@ -801,7 +825,6 @@ cudaError_t launch_paged_attn(const Pages& c, const void* Q, int Hq, const int32
     a.O = static_cast<uint16_t*>(O);
     a.lse = lse;
     a.pieces = pieces;
-    a.units = reinterpret_cast<int2*>(units);
     a.pre = pre;
     a.own = pre.splits > 0 ? pre.own : nullptr;
     a.flag = flag;
@@ -811,7 +834,7 @@ cudaError_t launch_paged_attn(const Pages& c, const void* Q, int Hq, const int32
         if (e == cudaSuccess) e = page_map(&vm, c, c.V, kPageRows);
         if (e != cudaSuccess) return e;
     }
-    const int grid = paged_ctas();
+    const int grid = kPgCtas;
     const cudaError_t e = c.half ? paged_pick<F16>(grid, km, vm, a, st) : paged_pick<Bf16>(grid, km, vm, a, st);
     if (e != cudaSuccess) return e;
     if (idx) return c.half ? join_pick<F16, true>(a, st) : join_pick<Bf16, true>(a, st);

@@ -63,9 +63,8 @@ cudaError_t launch_prefix(const Pages& c, const void* Q, int Hq, const int32_t* 
                           float* parts, PrefixParts* out, unsigned* flag, cudaStream_t st);
 
 int paged_ctas();  // CTAs of the paged attention's grid
-// units: [B * Hkv] pairs of int32
 cudaError_t launch_paged_attn(const Pages& c, const void* Q, int Hq, const int32_t* lens, const int32_t* idx,
                               const int32_t* kreq, int k_max, float scale, void* O, float* lse, float* pieces,
-                              int32_t* units, const PrefixParts& pre, unsigned* flag, cudaStream_t st);
+                              const PrefixParts& pre, unsigned* flag, cudaStream_t st);
 
 }  // namespace tsa
