@@ -422,9 +422,10 @@ typedef struct {
     tsa_paged_cache cache;
     const void* Q;              /* [B, Hq, d], contiguous */
     const int32_t* seq_lens;    /* [B], 0 <= len_b <= max_pages * page_size */
-    const int32_t* idx;         /* NULL: every row; else [B, Hkv, k_max] rows, entries < 0 skipped */
+    const int32_t* idx;         /* NULL: every row; else [B, Hkv, k_max] rows, entries < 0 skipped
+                                 * (a row listed twice counts twice) */
     const int32_t* k_per_seq;   /* [B] or NULL (= k_max): entries of idx used, min(k, len_b) of them */
-    void* O;                    /* [B, Hq, d] in dtype; 0 for a sequence without a row */
+    void* O;                    /* [B, Hq, d] in dtype, not over Q; 0 for a sequence without a row */
     float* lse;                 /* NULL or [B, Hq]: base-2 log-sum-exp of the scaled logits (-inf without a row) */
     int32_t Hq, k_max;
     int32_t prefix_len;         /* tsa_prefix_attn: the rows that the batch shares */

@@ -201,8 +201,15 @@ def test_binding_refusals(tsa):
     bad(tsa.qk_norm_rope_args, Q, k[:2], Q, k[:2])
     bad(tsa.qk_norm_rope_args, Q, None, Q, None, q_weight=torch.ones(128, dtype=torch.bfloat16))
     bad(tsa.qk_norm_rope_args, Q, None, Q, None, positions=lens.long(), inv_freq=f)
-    with pytest.raises(tsa.TsaError):  # an inv_freq of 12 rotates 24 elements: the C side refuses
-        tsa.qk_norm_rope(tsa.qk_norm_rope_args(Q, None, Q, None, positions=lens, inv_freq=f[:12]), stream=0)
+    # host tensors make arguments, but no call
+    a = tsa.qk_norm_rope_args(Q, None, Q, None, positions=lens, inv_freq=f)
+    bad(tsa.qk_norm_rope, a)
+    bad(tsa.qk_norm_rope, a, stream=0)
+    bad(tsa.paged_append, tsa.paged_append_args(c, k, k, lens, ws))
+    bad(tsa.paged_attn, tsa.paged_attn_args(c, Q, lens, Q.clone(), ws, **ok))
+    # the C side's refusals come through as they are: an inv_freq of 12 would rotate 24 elements
+    a = tsa.qk_norm_rope_args(Q, None, Q, None, positions=lens, inv_freq=f[:12])
+    assert tsa.lib().tsa_qk_norm_rope(ctypes.byref(a), None) == 1 and "rot_dim" in tsa.last_error()
 
 
 # ------------------------------------------------------------------ the oracle's pins

@@ -288,6 +288,44 @@ def test_prefix_that_grows_and_large_scores(cuda_dev):
     assert torch.equal(O[-1], clean) and not torch.isfinite(O[:-1]).all()
 
 
+def test_a_prefix_that_no_sequence_holds(cuda_dev):
+    B, Hq, Hkv, P = 30, 16, 8, 400
+    lens = [P - 1 - 3 * i for i in range(B)]
+    K, V, table = pages(lens, Hkv, 16, torch.bfloat16, seed=12, dev=cuda_dev)
+    Q = queries(B, Hq, torch.bfloat16, dev=cuda_dev)
+    # (the table is as wide as the prefix: (B - 1) * P * Hkv = 92,800 rows would be shared)
+    wide = torch.full((B, 26), -1, dtype=torch.int32, device=cuda_dev)
+    wide[:, :table.shape[1]] = table
+    assert torch.equal(attend(K, V, wide, Q, lens, prefix=P)[0], attend(K, V, wide, Q, lens)[0])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("gap", [17.0, 19.0, 23.0])
+def test_a_long_flat_tail_below_a_spike(cuda_dev, dt, gap):
+    """One row far above tens of thousands that are worth exp(-gap) of it each, below fp16's smallest
+    number, with values that do not cancel: together they are worth more than an output's rounding."""
+    n, B, Hq, Hkv = 40000, 4, 16, 2
+    one = torch.ones(128) / math.sqrt(128.0)
+    K = torch.zeros(n // 64, Hkv, 64, 128, dtype=DT[dt])
+    K[0, :, 5] = (one * 16).to(DT[dt])
+    V = torch.full((n // 64, Hkv, 64, 128), 1.0, dtype=DT[dt])
+    V[0, :, 5] = 0
+    K, V = K.to(cuda_dev), V.to(cuda_dev)
+    table = torch.arange(n // 64, dtype=torch.int32, device=cuda_dev).repeat(B, 1).contiguous()
+    # q . k = gap / SCALE for the spike
+    Q = (one * gap / SCALE / 16).to(DT[dt]).expand(B, Hq, 128).contiguous().to(cuda_dev)
+    lens = [n] * B
+    want, wl = oracle.paged_attn(Q[:1], K.cpu(), V.cpu(), table[:1].cpu(), lens[:1], SCALE)
+    for P in (None, n - 100):
+        O, lse = attend(K, V, table, Q, lens, prefix=P)
+        # every output is the tail's share of the weight: its relative error is the tail weights'
+        # (one value of all of them: their rounding to 8 or 11 bits does not average out over a prefix)
+        bits = WEIGHT_BITS[dt] if P is None else {"bf16": 9, "fp16": 11}[dt]
+        tol = (half_step(DT[dt]) + 2.0 ** -bits + 2.0 ** -14) * want + torch.finfo(DT[dt]).eps * torch.finfo(DT[dt]).tiny
+        assert (np.abs(O.double().cpu().numpy() - want) <= tol).all(), (P, O[0, 0, 0].item(), want[0, 0, 0])
+        check_lse(lse, np.broadcast_to(wl, (B, Hq)))
+
+
 def test_not_a_number_stays_in_its_row(cuda_dev):
     B, Hq, Hkv, P = 33, 16, 8, 384
     lens = [P + 20 + i for i in range(B)]
@@ -567,6 +605,18 @@ def test_interleaved_halves_of_one_buffer(cuda_dev):
     a, _ = attend(K, V, table, Q, lens)
     b, _ = attend(kv[:, 0], kv[:, 1], table, Q, lens)
     assert torch.equal(a, b)
+
+
+def test_many_sequences(cuda_dev):
+    """More sequences than one pass over the lengths takes, most of them short."""
+    rng = np.random.default_rng(5)
+    lens = [int(x) for x in rng.integers(0, 40, 1500)]
+    K, V, table = pages(lens, 1, 16, torch.float16, seed=10, dev=cuda_dev)
+    Q = queries(1500, 3, torch.float16, dev=cuda_dev)
+    O, lse = attend(K, V, table, Q, lens)
+    want, wl = oracle.paged_attn(Q, K.cpu(), V.cpu(), table.cpu(), lens, SCALE)
+    check_attn(O, want, torch.float16, 20, vmax(V))
+    check_lse(lse, wl)
 
 
 def test_no_sequence_and_no_row(cuda_dev):

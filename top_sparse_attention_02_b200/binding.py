@@ -343,9 +343,9 @@ def _launch(fn, a, stream):
     that device current.  (The raw queries below: a decode step makes many such calls of
     a few microseconds each, and torch's stream and device objects cost as much again.)"""
     i = a._index
-    if i is None or i == torch._C._cuda_getDevice():
-        raw = torch._C._cuda_getCurrentRawStream(i) if stream is None and i is not None else _stream(stream)
-        st = fn(ctypes.byref(a), raw)
+    _need(i is not None, "the tensors are not on a CUDA device")
+    if i == torch._C._cuda_getDevice():
+        st = fn(ctypes.byref(a), torch._C._cuda_getCurrentRawStream(i) if stream is None else _stream(stream))
     else:
         with torch.cuda.device(i):
             st = fn(ctypes.byref(a), _stream(stream))

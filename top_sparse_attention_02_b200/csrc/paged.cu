@@ -290,6 +290,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     // sequences: all at once, and the second pass finds them in registers)
     const int B = a.c.B, Hkv = a.c.Hkv;
     int cnt[4], total = 0;
+#pragma unroll 4
     for (int b0 = 0; b0 < B; b0 += 128) {
         slots4<GATHER>(a, b0, lane, cta == 0 && warp == 0, cnt);
         total += __reduce_add_sync(0xffffffffu, cnt[0] + cnt[1] + cnt[2] + cnt[3]);
@@ -593,7 +594,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
                         // (no row so far: the scores are -inf and the weights 0)
-                        const float ms[2] = {m[t][0] == kNegInf ? 0.f : m[t][0], m[t][1] == kNegInf ? 0.f : m[t][1]};
+                        const float ms[2] = {m[t][0] == kNegInf ? 0.f : m[t][0] - E::kBias, m[t][1] == kNegInf ? 0.f : m[t][1] - E::kBias};
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
                             // j = 0: rows 0-7, j = 1: rows 8-15; two heads each
@@ -637,7 +638,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                         const int head = t * 8 + (lane & 3) * 2 + j;
                         float* w = merge + (warp * Cfg::kHeads + head) * kPartFloats;
                         if (lane < 4) {
-                            w[kD] = m[t][j];
+                            w[kD] = m[t][j] - E::kBias;
                             w[kD + 1] = x;
                         }
 #pragma unroll

@@ -19,8 +19,15 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// The element types.  Softmax weights become elements for the second product; an fp16
+// one below 2^-25 is zero, and a long flat tail of such weights may be worth more
+// than an output's rounding.  So fp16 weights are formed relative to a maximum
+// lowered by a bias (their sums and the maximum kept with them are, too, and the
+// quotient is the same): kBias for weights of at most 1, and kBiasRef, kGrow for those
+// of a shared prefix, whose reference may fall 2^kGrow behind the maximum.
 struct Bf16 {
     static constexpr bool kHalf = false;
+    static constexpr float kBias = 0.f, kBiasRef = 0.f, kGrow = 8.f;
     static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
         uint32_t r;
         asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
@@ -46,6 +53,7 @@ struct Bf16 {
 
 struct F16 {
     static constexpr bool kHalf = true;
+    static constexpr float kBias = 12.f, kBiasRef = 10.f, kGrow = 5.f;  // weights up to 2^12, 2^15; below 2^-37, 2^-35: zero
     static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
         uint32_t r;
         asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));

@@ -21,8 +21,8 @@
 //            row took 1650 cycles a tile, longer than the other stream's products), the
 //            halves' maxima exchanged through shared memory; P = 2^(S - m) in 16 bits
 //            over S's columns, l in fp32.  O is rescaled in TMEM only when the maximum
-//            has grown by more than 2^8 (the result is the same: all sums are relative
-//            to the maximum they were formed with).
+//            has grown by more than 2^8 (fp16: 2^5; the result is the same: all sums
+//            are relative to the reference they were formed with).
 //   warp 19  only makes warps 16-19 a warpgroup that hands registers to the softmax
 //            (96 a thread at launch; 56 here and 104 there: 4 x 104 + 56 <= 5 x 96).
 // TMEM is full: 2 x (S 128 + O 128) columns.  When 128 rows or fewer are left for a
@@ -415,9 +415,10 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             if (!ok) continue;
             float mx = max3(maxima[row], maxima[kPxTile + row], -INFINITY) * a.scale_log2;
             // a NaN or an infinite score: the row's result is NaN, as the softmax's is
-            if (!(mx < INFINITY)) l = NAN, mx = m;
+            if (!(mx < INFINITY)) l = NAN, mx = -INFINITY;
             // rescale when some row's maximum has left the range that the sums were formed for
-            const bool grow = mx > m + 8.f || (m == -INFINITY && mx > m);
+            mx -= E::kBiasRef;
+            const bool grow = mx > m + E::kGrow || (m == -INFINITY && mx > m);
             if (__any_sync(0xffffffffu, grow)) {
                 const float f = grow ? (m == -INFINITY ? 0.f : ex2(m - mx)) : 1.f;
                 if (grow) m = mx;
