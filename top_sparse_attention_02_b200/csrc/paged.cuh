@@ -19,6 +19,26 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// ---- two fp32 values in one 64-bit register: one instruction for both
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;\n" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 // The element types.  Softmax weights become elements for the second product; an fp16
 // one below 2^-25 is zero, and a long flat tail of such weights may be worth more
 // than an output's rounding.  So fp16 weights are formed relative to a maximum
@@ -41,14 +61,20 @@ struct Bf16 {
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     }
-    static __device__ __forceinline__ void unpack8(const uint4& r, float (&f)[8]) {
-        f[0] = lo(r.x), f[1] = hi(r.x), f[2] = lo(r.y), f[3] = hi(r.y);
-        f[4] = lo(r.z), f[5] = hi(r.z), f[6] = lo(r.w), f[7] = hi(r.w);
+    static __device__ __forceinline__ void unpack8(const uint4& r, uint64_t (&f)[4]) {
+        f[0] = pack2(lo(r.x), hi(r.x)), f[1] = pack2(lo(r.y), hi(r.y));
+        f[2] = pack2(lo(r.z), hi(r.z)), f[3] = pack2(lo(r.w), hi(r.w));
     }
-    static __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-        return make_uint4(pack(f[0], f[1]), pack(f[2], f[3]), pack(f[4], f[5]), pack(f[6], f[7]));
+    static __device__ __forceinline__ uint4 pack8(const uint64_t (&f)[4]) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float a, b;
+            unpack2(f[j], a, b);
+            w[j] = pack(a, b);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
     }
-    static __device__ __forceinline__ uint16_t one(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
 };
 
 struct F16 {
@@ -67,14 +93,20 @@ struct F16 {
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     }
-    static __device__ __forceinline__ void unpack8(const uint4& r, float (&f)[8]) {
-        f[0] = lo(r.x), f[1] = hi(r.x), f[2] = lo(r.y), f[3] = hi(r.y);
-        f[4] = lo(r.z), f[5] = hi(r.z), f[6] = lo(r.w), f[7] = hi(r.w);
+    static __device__ __forceinline__ void unpack8(const uint4& r, uint64_t (&f)[4]) {
+        f[0] = pack2(lo(r.x), hi(r.x)), f[1] = pack2(lo(r.y), hi(r.y));
+        f[2] = pack2(lo(r.z), hi(r.z)), f[3] = pack2(lo(r.w), hi(r.w));
     }
-    static __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-        return make_uint4(pack(f[0], f[1]), pack(f[2], f[3]), pack(f[4], f[5]), pack(f[6], f[7]));
+    static __device__ __forceinline__ uint4 pack8(const uint64_t (&f)[4]) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float a, b;
+            unpack2(f[j], a, b);
+            w[j] = pack(a, b);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
     }
-    static __device__ __forceinline__ uint16_t one(float x) { return __half_as_ushort(__float2half_rn(x)); }
 };
 
 }  // namespace tsa

@@ -41,64 +41,72 @@ __device__ __forceinline__ float2 rope_angle(int pos, double inv_freq) {
     return make_float2(c, s);
 }
 
-// A lane's share of a token's rotation: x[j] -> x[j] * c[j] + partner * s[j].
+// A lane's share of a token's rotation and norm weights: x -> x * A + partner * B, two
+// elements an instruction, with the weights (of the element, of its partner) in A and B.
 template <bool INTER>
 struct LaneRot {
-    float c[8], s[8];
+    uint64_t A[4], B[4];
     int src;  // split pairs: the lane (of 32) that holds the partners
     bool on;  // this lane's elements are rotated
-    __device__ __forceinline__ void off(int lane) {
-        on = false;
-        src = lane;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) c[j] = 1.f, s[j] = 0.f;
+    float w[8], wp[8];  // the weights of this lane's elements and of their partners (dead once A and B are made)
+    __device__ __forceinline__ LaneRot(const Rotation& rot, int lane) {
+        const int l = lane & 15, h = rot.rot_dim >> 4;  // h: lanes of half a rotated head
+        on = l < 2 * h;
+        src = INTER || !on ? lane : l < h ? lane + h : lane - h;
     }
-    // all lanes; cs: kD / 2 angles of this warp's in shared memory
-    __device__ __forceinline__ void load(float2* cs, int pos, const Rotation& rot, int lane) {
-        const int half = rot.rot_dim >> 1;
-        for (int f = lane; f < half; f += 32) cs[f] = rope_angle(pos, rot.inv_freq[f]);
-        __syncwarp();
-        const int l = lane & 15, h = rot.rot_dim >> 4;  // lanes of half a rotated head
-        if (l >= 2 * h) return;
-        on = true;
-        if (INTER) {
+    // the heads' weights [kD], or NULL; requested early
+    __device__ __forceinline__ void weights(const float* weight, int lane) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 v = cs[l * 4 + j];
-                c[2 * j] = c[2 * j + 1] = v.x;
-                s[2 * j] = -v.y;
-                s[2 * j + 1] = v.y;
-            }
-        } else {
-            const bool low = l < h;
-            src = low ? lane + h : lane - h;
-            const int i0 = (low ? l : l - h) * 8;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float2 v = cs[i0 + j];
-                c[j] = v.x;
-                s[j] = low ? -v.y : v.y;
+        for (int j = 0; j < 8; j += 4) {
+            const float4 one = make_float4(1.f, 1.f, 1.f, 1.f);
+            const float4 v = weight ? *reinterpret_cast<const float4*>(weight + (lane & 15) * 8 + j) : one;
+            w[j] = v.x, w[j + 1] = v.y, w[j + 2] = v.z, w[j + 3] = v.w;
+            if (!INTER) {
+                const float4 p = weight ? *reinterpret_cast<const float4*>(weight + (src & 15) * 8 + j) : one;
+                wp[j] = p.x, wp[j + 1] = p.y, wp[j + 2] = p.z, wp[j + 3] = p.w;
             }
         }
     }
-    __device__ __forceinline__ void apply(float (&x)[8]) const {  // all lanes
-        if (INTER) {
-            if (!on) return;
+    // cs: the token's kD / 2 angles
+    __device__ __forceinline__ void coefficients(const float2* cs, const Rotation& rot, int lane) {
+        const int l = lane & 15, h = rot.rot_dim >> 4;
+        const bool low = l < h;
+        const int i0 = INTER ? l * 4 : (low ? l : l - h) * 8;
 #pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-                const float a = x[j], b = x[j + 1];
-                x[j] = fmaf(b, s[j], a * c[j]);
-                x[j + 1] = fmaf(a, s[j + 1], b * c[j + 1]);
+        for (int j = 0; j < 8; j += 2) {
+            float2 v[2] = {make_float2(1.f, 0.f), make_float2(1.f, 0.f)};
+            if (on) {
+                v[0] = cs[INTER ? i0 + j / 2 : i0 + j];
+                v[1] = INTER ? v[0] : cs[i0 + j + 1];
             }
-        } else {
+            A[j / 2] = pack2(v[0].x * w[j], v[1].x * w[j + 1]);
+            // (interleaved: a lane's first of a pair is turned by -sin of the second, the second by sin of the first)
+            B[j / 2] = INTER ? pack2(-v[0].y * w[j + 1], v[1].y * w[j])
+                             : pack2((low ? -v[0].y : v[0].y) * wp[j], (low ? -v[1].y : v[1].y) * wp[j + 1]);
+        }
+    }
+    __device__ __forceinline__ void apply(uint64_t (&x)[4]) const {  // all lanes
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float p = __shfl_sync(0xffffffffu, x[j], src);
-                if (on) x[j] = fmaf(p, s[j], x[j] * c[j]);
+        for (int j = 0; j < 4; ++j) {
+            float x0, x1;
+            unpack2(x[j], x0, x1);
+            uint64_t p;
+            if (INTER) {
+                p = pack2(x1, x0);
+            } else {
+                p = pack2(__shfl_sync(0xffffffffu, x0, src), __shfl_sync(0xffffffffu, x1, src));
             }
+            x[j] = mul2(x[j], A[j]);
+            if (on) x[j] = fma2(p, B[j], x[j]);
         }
     }
 };
+
+// the token's angles into this warp's shared memory
+__device__ __forceinline__ void token_angles(float2* cs, int pos, const Rotation& rot, int lane) {
+    for (int f = lane; f < rot.rot_dim >> 1; f += 32) cs[f] = rope_angle(pos, rot.inv_freq[f]);
+    __syncwarp();
+}
 
 // The heads of one token, two at a time: pairs first, first + step, ... of H heads
 // at src + h * sh, through fn(raw) into dst + h * dh.  The first loads are issued
@@ -107,34 +115,36 @@ struct HeadWalk {
     const uint16_t* src;
     uint16_t* dst;
     long long sh, dh;
-    int H, step, h;  // h: this lane's head of the next pair
+    int H, step, pair, odd;  // pair: the next one (the whole warp's); odd: this half-warp's head of a pair
     uint4 raw[kRopePairs];
     __device__ __forceinline__ HeadWalk(const void* s, long long soff, long long sh_, void* d, long long doff,
                                         long long dh_, int H_, int first, int step_, int lane)
-        : sh(sh_), dh(dh_), H(H_), step(2 * step_), h(2 * first + (lane >> 4)) {
-        src = static_cast<const uint16_t*>(s) + soff + (lane & 15) * 8;
-        dst = static_cast<uint16_t*>(d) + doff + (lane & 15) * 8;
+        : H(H_), step(step_), pair(first), odd(lane >> 4) {
+        src = static_cast<const uint16_t*>(s) + soff + odd * sh_ + (lane & 15) * 8;
+        dst = static_cast<uint16_t*>(d) + doff + odd * dh_ + (lane & 15) * 8;
+        sh = 2 * sh_;
+        dh = 2 * dh_;
         fetch();
     }
     __device__ __forceinline__ void fetch() {
 #pragma unroll
         for (int u = 0; u < kRopePairs; ++u) {
-            const int hu = h + u * step;
-            raw[u] = hu < H ? *reinterpret_cast<const uint4*>(src + hu * sh) : make_uint4(0, 0, 0, 0);
+            const int p = pair + u * step;
+            raw[u] = make_uint4(0, 0, 0, 0);
+            if (2 * p + odd < H) raw[u] = *reinterpret_cast<const uint4*>(src + p * sh);
         }
     }
     template <class F>
-    __device__ __forceinline__ void run(F fn) {
-        // (h of the even lanes' head decides for the warp: fn shuffles)
-        while (__any_sync(0xffffffffu, h < H)) {
+    __device__ __forceinline__ void run(F fn) {  // all lanes together: fn shuffles
+        while (2 * pair < H) {
 #pragma unroll
             for (int u = 0; u < kRopePairs; ++u) {
-                const int hu = h + u * step;
-                if (u && !__any_sync(0xffffffffu, hu < H)) break;
+                const int p = pair + u * step;
+                if (u && 2 * p >= H) break;
                 const uint4 y = fn(raw[u]);
-                if (hu < H) *reinterpret_cast<uint4*>(dst + hu * dh) = y;
+                if (2 * p + odd < H) *reinterpret_cast<uint4*>(dst + p * dh) = y;
             }
-            h += kRopePairs * step;
+            pair += kRopePairs * step;
             fetch();
         }
     }
@@ -160,34 +170,37 @@ qk_norm_rope_kernel(Heads q, Heads k, Heads qo, Heads ko, int T, int Hq, int Hkv
     if (!rope_place(T, W, &t, &w)) return;
     const int pos = rot.rot_dim > 0 ? positions[t] : 0;
     HeadWalk hq(q.p, t * q.st, q.sh, const_cast<void*>(qo.p), t * qo.st, qo.sh, Hq, w, W, lane);
-    LaneRot<INTER> lr;
-    lr.off(lane);
-    if (rot.rot_dim > 0) lr.load(cs[threadIdx.x >> 5], pos, rot, lane);
+    LaneRot<INTER> lr(rot, lane);
+    lr.weights(wq, lane);
+    token_angles(cs[threadIdx.x >> 5], pos, rot, lane);
     auto heads = [&](HeadWalk& hw, const float* weight) {
-        float wv[8];
-        if (weight) {
-            const float4 w0 = *reinterpret_cast<const float4*>(weight + (lane & 15) * 8);
-            const float4 w1 = *reinterpret_cast<const float4*>(weight + (lane & 15) * 8 + 4);
-            wv[0] = w0.x, wv[1] = w0.y, wv[2] = w0.z, wv[3] = w0.w, wv[4] = w1.x, wv[5] = w1.y, wv[6] = w1.z, wv[7] = w1.w;
-        }
+        lr.coefficients(cs[threadIdx.x >> 5], rot, lane);
         hw.run([&](const uint4& raw) {
-            float x[8];
+            uint64_t x[4];
             E::unpack8(raw, x);
+            float r = 1.f;
             if (weight) {
-                float ss = 0.f;
+                uint64_t sq = mul2(x[0], x[0]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
+                for (int j = 1; j < 4; ++j) sq = fma2(x[j], x[j], sq);
+                float s0, s1;
+                unpack2(sq, s0, s1);
+                float ss = s0 + s1;
 #pragma unroll
                 for (int m = 1; m < 16; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-                const float r = rsqrtf(fmaf(ss, 1.0f / kD, eps));
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = x[j] * r * wv[j];
+                r = rsqrtf(fmaf(ss, 1.0f / kD, eps));
             }
             lr.apply(x);
+            if (weight) {
+                const uint64_t rr = pack2(r, r);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = mul2(x[j], rr);
+            }
             return E::pack8(x);
         });
     };
     heads(hq, wq);
+    lr.weights(wk, lane);
     // the keys' pairs go on where the queries' ended, so that the warps share them evenly
     const int pq = (Hq + 1) / 2, fk = (w + W - pq % W) % W;
     HeadWalk hk(k.p, t * k.st, k.sh, const_cast<void*>(ko.p), t * ko.st, ko.sh, Hkv, fk, W, lane);
@@ -225,11 +238,12 @@ paged_append_kernel(Pages c, Heads k, Heads v, int T, const int32_t* __restrict_
     hk.dst += at;
     hv.dst += at;
     hv.run([](const uint4& raw) { return raw; });
-    LaneRot<INTER> lr;
-    lr.off(lane);
-    if (rot.rot_dim > 0) lr.load(cs[threadIdx.x >> 5], pos, rot, lane);
+    token_angles(cs[threadIdx.x >> 5], pos, rot, lane);
+    LaneRot<INTER> lr(rot, lane);
+    lr.weights(nullptr, lane);
+    lr.coefficients(cs[threadIdx.x >> 5], rot, lane);
     hk.run([&](const uint4& raw) {
-        float x[8];
+        uint64_t x[4];
         E::unpack8(raw, x);
         lr.apply(x);
         return lr.on ? E::pack8(x) : raw;  // unrotated elements bit by bit
