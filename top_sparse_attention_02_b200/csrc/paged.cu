@@ -19,8 +19,7 @@
 //    kernel joins the pieces of each row (with a shared prefix's partials, where
 //    there is one), in the order of the CTAs, so that the result does not depend on
 //    who was last.  (The last CTA of a unit to arrive, found by a counter, took 3.8 us
-//    from its piece to O; the second kernel, which by then is resident and has
-//    found where its pieces lie, takes 3, and leaves no counter to keep at zero.)
+//    from its piece to O; a first form of the second kernel, which by then is resident, 3.5.)
 //  - Each of a CTA's 4 warps streams its own 16 rows of every granule through
 //    its own ring of 8 KB stages (K and V of 16 rows), so a warp never waits for
 //    another one until the unit ends.  Two CTAs an SM.  Every row: two 2-D boxes
@@ -38,7 +37,7 @@
 // 6.45 TB/s, HBM's rate; 17 ragged sequences, 40/8 heads, 139 MB 28.2 us = 4.9 TB/s; one
 // sequence of 4096 rows, 2 kv-heads 8.2 us; 2621 selected rows of 8 kv-heads at 131072 (10.7 MB)
 // 9.9 us.  The last two are a chain of waits: lengths 0.9 us, pages (or list, then pages) 1 to 2,
-// rows 0.4, products and the warps' merge 1.5, then the second kernel 3.
+// rows 0.4, products and the warps' merge 1.5 (marks of SM time); the second kernel is the rest.
 //
 // Rows outside the sequence in a tile that is partly valid: their scores become
 // -inf, and their V rows are overwritten with zeros in shared memory (0 * NaN in
@@ -60,7 +59,7 @@ constexpr int kPgStage = 4 * kPgHalf;              // K halves, V halves: 8 KB
 constexpr int kPgCtasPerSm = 2;
 constexpr int kPgCtas = kPgCtasPerSm * kPagedSms;  // the grid
 constexpr int kPgPieces = 64;  // pieces of a unit that one round of loads joins (8 warps, 8 loads each)
-constexpr int kPgEnd = 1;      // empty slots after a unit (17 ragged sequences: none 38.2 us, one 30.8, two 29.6; 400 short: 71, 58.5, 59)
+constexpr int kPgEnd = 1;      // empty slots after a unit (17 ragged sequences: none 37.5 us, one 29.9, two 29.6; 400 short ones: 71, 58.5, 59.1)
 constexpr int kPgLong = 8;     // granules a CTA above which more pieces pay
 constexpr float kNegInf = -INFINITY;
 

@@ -33,13 +33,12 @@
 // long.  The outputs' error is then 1.4 times their own rounding's (2.3e-3 against 1.7e-3 of
 // the norm in bf16), the weights' errors being independent.
 //
-// Measured: 64 sequences x 64/8 heads over 32768 rows (68.7 Gflop, 134 MB) 77 us = 0.9 PFLOP/s,
-// 0.54 of the measured matrix rate.  A pair of tiles takes 3870 cycles where their products take
-// 2068: each stream is a chain of softmax (2150: load 155, maximum 380, exchange and check 400, the
-// weights 1250, of which the special-function units need 1024, store 100), turn and products
-// (1700), and TMEM has no room for S of a third tile.  Half tiles (64 columns) with S two
+// Measured: 64 sequences x 64/8 heads over 32768 rows (68.7 Gflop, 134 MB) 79 us with the join = 0.87 PFLOP/s,
+// 0.53 of the measured matrix rate.  A pair of tiles takes 3870 cycles where their products take
+// 2068: each stream is a chain of softmax (2150, of which the special-function units need
+// 1024), turn, products and their waits (1700), and TMEM has no room for S of a third tile.  Half tiles (64 columns) with S two
 // halves ahead came to 4140 (one thread a row) and 3870 (two groups in turn); a part of the
-// weights by polynomial on the FMA pipe, packed arithmetic, the maximum beside
+// weights by polynomial on the FMA pipe, the maximum found beside
 // the weights and a staggered start changed nothing or were slower.
 //
 // Sequences shorter than the prefix have rows here, too, which nobody reads: no row

@@ -18,14 +18,14 @@
 // positions), keeps them in registers, and goes through the token's heads with
 // four pairs of loads in flight.  Few tokens are split by heads over more warps.
 // (A CTA of 256 threads that shared the angles of 4 tokens through a barrier, in
-// 110 registers, took twice as long: too few warps an SM, all waiting for the angles.)
+// 110 registers, took 72 us for the first of the cases below.)
 //
 // Measured: 8192 tokens x 40 heads, split pairs (168 MB) 34 us = 4.9 TB/s, where a plain
 // copy of those bytes takes 27; 4099 x 72 heads, interleaved (151 MB) 26.5 us = 5.7 TB/s;
 // appending 16348 tokens of 8 + 8 heads (134 MB) 22.6 us = 5.9 TB/s; one token 2.8 us, a
-// launch.  Split pairs are bound by issue (67% of the slots; 140 instructions a pair
-// of heads, the partners' shuffles among them), the others by HBM.  Refilling each load as it is used
-// (three more registers' worth) or walking by pointers cost more in occupancy than they saved.
+// launch.  A plain copy of 67 to 84 MB runs at 6.0 to 6.1 TB/s.  Split pairs use 67% of the
+// issue slots (140 instructions a pair of heads, the partners' shuffles among them) and
+// 43% of HBM.  Walking the heads by pointers instead of indexes took 37.8 and 33.9 us.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
