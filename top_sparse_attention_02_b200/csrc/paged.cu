@@ -33,8 +33,8 @@
 //    keep about 16 bits and the output's own rounding is the larger error; the
 //    second product costs little in a kernel that waits for memory.
 //
-// Measured (graph replays): 64 sequences of 8192 to 32768 rows, 64/8 heads (5.18 GB) 803 us =
-// 6.45 TB/s, HBM's rate; 17 ragged sequences, 40/8 heads, 139 MB 28.2 us = 4.9 TB/s; one
+// Measured (graph replays): 64 sequences of 8192 to 32768 rows, 64/8 heads (5.18 GB) 805 us =
+// 6.44 TB/s, HBM's rate; 17 ragged sequences, 40/8 heads, 139 MB 28.5 us = 4.9 TB/s; one
 // sequence of 4096 rows, 2 kv-heads 8.2 us; 2621 selected rows of 8 kv-heads at 131072 (10.7 MB)
 // 9.9 us.  The last two are a chain of waits: lengths 0.9 us, pages (or list, then pages) 1 to 2,
 // rows 0.4, products and the warps' merge 1.5 (marks of SM time); the second kernel is the rest.
@@ -780,14 +780,16 @@ static cudaError_t join_launch(const PgArgs& a, cudaStream_t st) {
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// The fewer rows, the more warps each: 8 (a row of 64 pieces: one round of loads), 4
-// while that fills the SMs once (256 rows of 17 partials 3.6 us, against 7.5 with
-// one), then one (4096 rows of 10: 7.1 us, against 17 with four).
+// The fewer rows, the more warps each, as long as the CTAs (8 warps) come to two an SM.
+// The whole call with 1, 4 and 8 warps a row, us: 8 rows of 60 pieces 16.3, 10.0, 8.2;
+// 256 rows of a shared prefix 20.6, 18.8, 18.9; 320 rows of it 21.2, 19.2, 21.6; 512 rows
+// (a prefix of 16384) 35.8, 28.9, 33.4; 768 rows 26.2, 26.6, 30.3, and without a prefix
+// 37.7, 41.5, 44.3; 1024 rows 30.1, 33.4, 38.4; 4096 rows 121.7, 136, 157.
 template <class E, bool GATHER>
 static cudaError_t join_pick(const PgArgs& a, cudaStream_t st) {
     const long long rows = (long long)a.c.B * a.Hq;
     if (rows <= 2 * kPagedSms) return join_launch<E, 8, GATHER>(a, st);
-    if (rows <= 8 * kPagedSms) return join_launch<E, 4, GATHER>(a, st);
+    if (rows <= 4 * kPagedSms) return join_launch<E, 4, GATHER>(a, st);
     return join_launch<E, 1, GATHER>(a, st);
 }
 
