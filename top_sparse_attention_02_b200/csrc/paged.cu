@@ -575,7 +575,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) s[t][j] = (j < 2 ? v0 : v1) ? (s[t][j] + s2[t][j]) * a.scale_log2 : kNegInf;
+                        for (int j = 0; j < 4; ++j) s[t][j] = (j < 2 ? v0 : v1) ? __fmul_rn(s[t][j] + s2[t][j], a.scale_log2) : kNegInf;
                         up |= fmaxf(s[t][0], s[t][2]) > m[t][0] || fmaxf(s[t][1], s[t][3]) > m[t][1];
                     }
                     if (__any_sync(0xffffffffu, up)) {  // a larger maximum: rescale what there is
@@ -588,7 +588,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
                                 x = fmaxf(x, m[t][j]);
-                                const float f = x == kNegInf ? 1.f : exp2f(m[t][j] - x);
+                                const float f = x == kNegInf ? 1.f : exp2f(lowered<E>(m[t][j]) - lowered<E>(x));
                                 m[t][j] = x;
                                 l[t][j] *= f;
 #pragma unroll
@@ -600,7 +600,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
                         // (no row so far: the scores are -inf and the weights 0)
-                        const float ms[2] = {m[t][0] == kNegInf ? 0.f : m[t][0] - E::kBias, m[t][1] == kNegInf ? 0.f : m[t][1] - E::kBias};
+                        const float ms[2] = {m[t][0] == kNegInf ? 0.f : lowered<E>(m[t][0]), m[t][1] == kNegInf ? 0.f : lowered<E>(m[t][1])};
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
                             // j = 0: rows 0-7, j = 1: rows 8-15; two heads each
@@ -644,7 +644,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                         const int head = t * 8 + (lane & 3) * 2 + j;
                         float* w = merge + (warp * Cfg::kHeads + head) * kPartFloats;
                         if (lane < 4) {
-                            w[kD] = m[t][j] - E::kBias;
+                            w[kD] = lowered<E>(m[t][j]);
                             w[kD + 1] = x;
                         }
 #pragma unroll

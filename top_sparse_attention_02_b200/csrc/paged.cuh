@@ -45,6 +45,15 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 // lowered by a bias (their sums and the maximum kept with them are, too, and the
 // quotient is the same): kBias for weights of at most 1, and kBiasRef, kGrow for those
 // of a shared prefix, whose reference may fall 2^kGrow behind the maximum.
+//
+// From 2^22 on (base 2) a step of fp32 is 1/2 and more: a maximum of 2^27 less 12 rounds to
+// it less 16, and a product that is not rounded may lie several above its maximum, which
+// was.  Such maxima are not lowered, and their scores are rounded before anything is
+// taken from them, so that no weight exceeds 1 (in fp16 one of 2^16 would be infinite).
+constexpr float kBigLogit = 4194304.f;
+template <class E>
+__device__ __forceinline__ float lowered(float m) { return fabsf(m) < kBigLogit ? m - E::kBias : m; }
+
 struct Bf16 {
     static constexpr bool kHalf = false;
     static constexpr float kBias = 0.f, kBiasRef = 0.f, kGrow = 8.f;

@@ -425,12 +425,13 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             // both halves have their S in registers (P goes over it) and each other's maximum
             asm volatile("bar.sync %0, 256;\n" ::"r"(2 + s) : "memory");
             if (!ok) continue;
-            float mx = max3(maxima[row], maxima[kPxTile + row], -INFINITY) * a.scale_log2;
+            float mx = __fmul_rn(max3(maxima[row], maxima[kPxTile + row], -INFINITY), a.scale_log2);
             // a NaN or an infinite score: the row's result is NaN, as the softmax's is
             if (!(mx < INFINITY)) l = NAN, mx = -INFINITY;
             // rescale when some row's maximum has left the range that the sums were formed for
-            mx -= E::kBiasRef;
-            const bool grow = mx > m + E::kGrow || (m == -INFINITY && mx > m);
+            const bool big = fabsf(mx) >= kBigLogit && mx > -INFINITY;  // (no fraction left: see kBigLogit)
+            if (!big) mx -= E::kBiasRef;
+            const bool grow = mx > m + (big ? 0.f : E::kGrow) || (m == -INFINITY && mx > m);
             if (__any_sync(0xffffffffu, grow)) {
                 const float f = grow ? (m == -INFINITY ? 0.f : ex2(m - mx)) : 1.f;
                 if (grow) m = mx;
@@ -466,8 +467,10 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                     // (a quarter of these by polynomial on the FMA pipe, packed or not, took as long)
-                    const float p0 = ex2(fmaf(__uint_as_float(x[c][2 * j]), a.scale_log2, shift));
-                    const float p1 = ex2(fmaf(__uint_as_float(x[c][2 * j + 1]), a.scale_log2, shift));
+                    // (the product is rounded as the maximum's was: a fused one may lie above it by half a
+                    // step of the score, 2^4 at 2^28; that would save 2 us of the large batch's 124)
+                    const float p0 = ex2(__fmul_rn(__uint_as_float(x[c][2 * j]), a.scale_log2) + shift);
+                    const float p1 = ex2(__fmul_rn(__uint_as_float(x[c][2 * j + 1]), a.scale_log2) + shift);
                     ls[2 * j & 3] += p0;
                     ls[(2 * j & 3) + 1] += p1;
                     p[j] = E::pack(p0, p1);
