@@ -1,0 +1,37 @@
+"""What the paged kernels' sources promise and a run may not show."""
+import glob
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "top_sparse_attention_02_b200", "csrc")
+
+
+def kernels(path):
+    """(name, parameters, body) of each kernel of a source file."""
+    src = re.sub(r"//[^\n]*", "", open(path).read())
+    for m in re.finditer(r"__global__\s+void\s+(?:__launch_bounds__\([^)]*\)\s+)?(\w+)\s*\(", src):
+        at, depth = m.end(), 1
+        while depth:
+            depth += {"(": 1, ")": -1}.get(src[at], 0)
+            at += 1
+        params, body, depth = src[m.end():at - 1], src.index("{", at), 1
+        end = body + 1
+        while depth:
+            depth += {"{": 1, "}": -1}.get(src[end], 0)
+            end += 1
+        yield m.group(1), params, src[body:end]
+
+
+@pytest.mark.parametrize("name", ["rope.cu", "paged.cu", "prefix.cu"])
+def test_inputs_that_the_kernel_before_may_write_are_not_restrict(name):
+    """A kernel that starts while the one before still runs must not promise the compiler that
+    its inputs stay unchanged for as long as it runs."""
+    found = 0
+    for kernel, params, body in kernels(os.path.join(CSRC, name)):
+        assert "griddep_wait" in body, kernel
+        found += 1
+        for p in params.split(","):
+            assert not ("const" in p and "__restrict__" in p), f"{kernel}: {p.strip()}"
+    assert found

@@ -164,10 +164,14 @@ __device__ __forceinline__ bool rope_place(int T, int W, int* t, int* w) {
     return *t < T;
 }
 
+// The kernel before may write any input (a decode loop advances its positions and rows on
+// the device) and may still run when this one starts.  So the inputs are plain pointers: as
+// __restrict__ to const they would be taken for unchanged while the kernel runs, and the
+// compiler could read them ahead of the wait, or through the cache that is not coherent.
 template <class E, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads)
-qk_norm_rope_kernel(Heads q, Heads k, Heads qo, Heads ko, int T, int Hq, int Hkv, const float* __restrict__ wq,
-                    const float* __restrict__ wk, float eps, const int32_t* __restrict__ positions, Rotation rot, int W) {
+qk_norm_rope_kernel(Heads q, Heads k, Heads qo, Heads ko, int T, int Hq, int Hkv, const float* wq,
+                    const float* wk, float eps, const int32_t* positions, Rotation rot, int W) {
     __shared__ float2 cs[kRopeWarps][kD / 2];
     griddep_wait();
     griddep_launch();
@@ -215,8 +219,8 @@ qk_norm_rope_kernel(Heads q, Heads k, Heads qo, Heads ko, int T, int Hq, int Hkv
 
 template <class E, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads)
-paged_append_kernel(Pages c, Heads k, Heads v, int T, const int32_t* __restrict__ seq, const int32_t* __restrict__ row,
-                    const int32_t* __restrict__ positions, Rotation rot, unsigned* __restrict__ flag, int W) {
+paged_append_kernel(Pages c, Heads k, Heads v, int T, const int32_t* seq, const int32_t* row,
+                    const int32_t* positions, Rotation rot, unsigned* flag, int W) {
     __shared__ float2 cs[kRopeWarps][kD / 2];
     griddep_wait();
     griddep_launch();
