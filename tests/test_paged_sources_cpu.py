@@ -1,4 +1,4 @@
-"""What the paged kernels' sources promise and a run may not show."""
+"""What the kernels' sources promise and a run may not show."""
 import glob
 import os
 import re
@@ -24,14 +24,15 @@ def kernels(path):
         yield m.group(1), params, src[body:end]
 
 
-@pytest.mark.parametrize("name", ["rope.cu", "paged.cu", "prefix.cu"])
+@pytest.mark.parametrize("name", sorted(os.path.basename(p) for p in glob.glob(os.path.join(CSRC, "*.cu"))))
 def test_inputs_that_the_kernel_before_may_write_are_not_restrict(name):
     """A kernel that starts while the one before still runs must not promise the compiler that
     its inputs stay unchanged for as long as it runs."""
-    found = 0
+    waits = 0
     for kernel, params, body in kernels(os.path.join(CSRC, name)):
-        assert "griddep_wait" in body, kernel
-        found += 1
+        if "griddep_wait" not in body:
+            continue
+        waits += 1
         for p in params.split(","):
             assert not ("const" in p and "__restrict__" in p), f"{kernel}: {p.strip()}"
-    assert found
+    assert waits or name not in ("rope.cu", "paged.cu", "prefix.cu", "attn.cu", "topk.cu")

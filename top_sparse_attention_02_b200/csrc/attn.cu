@@ -400,9 +400,9 @@ __device__ __forceinline__ void warp_rows(const unsigned (&kt)[R], const unsigne
 template <int G, int STAGES, bool CLUSTER, bool CONTIG, bool ASYNC>
 __global__ void __launch_bounds__(kAttnThreads, ASYNC ? 2 : 1)
 attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-            const __nv_bfloat16* __restrict__ Q, const __nv_bfloat16* __restrict__ K,
-            const __nv_bfloat16* __restrict__ V, const int32_t* __restrict__ lens,
-            const int32_t* __restrict__ idx, const int32_t* __restrict__ kreq, int k_max,
+            const __nv_bfloat16* Q, const __nv_bfloat16* K,
+            const __nv_bfloat16* V, const int32_t* lens,
+            const int32_t* idx, const int32_t* kreq, int k_max,
             int block, int Hkv, int Ncap, float scale_log2, int S, float* __restrict__ part,
             unsigned* __restrict__ counters, float* __restrict__ O, unsigned* __restrict__ flag, int early,
             float* __restrict__ sout, float scale, float* __restrict__ lse, int work,

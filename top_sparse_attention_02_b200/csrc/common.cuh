@@ -79,7 +79,8 @@ __device__ __forceinline__ void halfwarp_reduce_scatter16(float (&v)[16], int c)
 // that the next one may start (launch, set-up) while this one finishes.  Every
 // kernel waits for its predecessor before touching global memory, which keeps
 // the stream's order for data; and lets its successor launch once all of its
-// CTAs are running.
+// CTAs are running.  Inputs of such a kernel are not __restrict__ to const: they change
+// while it runs, and the compiler could move their loads ahead of the wait.
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 __device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 

@@ -22,8 +22,8 @@ constexpr int kScoreWarps = kScoreThreads / 32;
 
 template <int G>
 __global__ void __launch_bounds__(kScoreThreads)
-score_kernel(const __nv_bfloat16* __restrict__ Q, const float* __restrict__ means,
-             const int32_t* __restrict__ lens, int Hkv, int Ncap, int rows_cap, int block,
+score_kernel(const __nv_bfloat16* Q, const float* means,
+             const int32_t* lens, int Hkv, int Ncap, int rows_cap, int block,
              float scale, float* __restrict__ scores, uint32_t* __restrict__ hist,
              unsigned* __restrict__ flag) {
     constexpr int R = 16 / G;          // rows per half-warp (R*G = 16 partial dots)

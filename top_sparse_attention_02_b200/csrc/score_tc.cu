@@ -109,8 +109,8 @@ __device__ __forceinline__ bool tc_wait(unsigned bar, unsigned parity, unsigned*
 
 template <int G>
 __global__ void __launch_bounds__(kTcThreads, 2)
-score_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __nv_bfloat16* __restrict__ Q,
-                const int32_t* __restrict__ lens, int Hkv, int Ncap, float scale,
+score_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __nv_bfloat16* Q,
+                const int32_t* lens, int Hkv, int Ncap, float scale,
                 float* __restrict__ scores, uint32_t* __restrict__ hist, int tiles_per_cta,
                 unsigned* __restrict__ flag, int early) {
     extern __shared__ unsigned char tc_smem_raw[];

@@ -72,8 +72,8 @@ __device__ __forceinline__ uint32_t block_excl_scan(uint32_t x, uint32_t* wsum, 
 }
 
 __global__ void __launch_bounds__(kTkThreads, 1)
-topk_kernel(const float* __restrict__ scores, const int32_t* __restrict__ lens,
-            const int32_t* __restrict__ kreq, int k_max, int Hkv, int Ncap, int rows_cap, int block,
+topk_kernel(const float* scores, const int32_t* lens,
+            const int32_t* kreq, int k_max, int Hkv, int Ncap, int rows_cap, int block,
             int chunk, int32_t* __restrict__ idx, unsigned* __restrict__ flag) {
     cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks();

@@ -89,8 +89,8 @@ __device__ __forceinline__ uint32_t th_block_scan(uint32_t x, uint32_t* wsum, ui
 
 template <int KPT>
 __global__ void __launch_bounds__(kThThreads, 1)
-topk_hist_kernel(const float* __restrict__ scores, const int32_t* __restrict__ lens,
-                 const int32_t* __restrict__ kreq, int k_max, int Hkv, int Ncap, int rows_cap, int block,
+topk_hist_kernel(const float* scores, const int32_t* lens,
+                 const int32_t* kreq, int k_max, int Hkv, int Ncap, int rows_cap, int block,
                  int32_t* __restrict__ idx, uint32_t* __restrict__ hist, unsigned* __restrict__ flag) {
     constexpr int kSeg = 32 * KPT;             // a warp's run of rows
     constexpr int kChunk = kThWarps * kSeg;    // a CTA's rows
