@@ -703,79 +703,98 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 // whose unit lay in one CTA, without a prefix, is in O already; a sequence without a
 // row gets zeros.  W warps a row, each with a part of the partials, whose loads are
 // all on their way at once.
+//
+// Each CTA adds up all lengths, so past kJoinCtas of them a CTA takes several blocks of
+// rows in turn: with a CTA for every 8 rows the additions grew with the square of the batch.
+// The whole call, us, at 592, 1184, 2368 CTAs and without a limit: 65536 sequences of 16
+// rows (8/1 heads) 1409, 1430, 1503, 5477; 4096 of 64 rows (32/8 heads) 327, 326, 330, 402;
+// 256 of 612 rows over a prefix of 512 (64/8) 64.0, 62.6, 62.6, 62.7.
 constexpr int kJoinWarps = 8;
-template <class E, int W, bool GATHER>
+constexpr int kJoinCtas = 8 * kPagedSms;
+template <class E, int W, bool GATHER, bool MANY>
 __global__ void __launch_bounds__(32 * kJoinWarps)
 paged_join_kernel(const PgArgs a, int rows) {
     __shared__ float wts[kJoinWarps][kMaxPrefixSplits + kPgCtas];
     __shared__ float4 sums[kJoinWarps][32];
     __shared__ int2 red[kJoinWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = warp % W;
-    const int row = blockIdx.x * (kJoinWarps / W) + warp / W;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float M = kNegInf, L = 0.f;
-    bool mine = row < rows;
-    // Where the row's pieces lie follows from the lengths, which the kernels before this
-    // one only read: found before the wait on them.
-    const int b = min(row, rows - 1) / a.Hq, r = min(row, rows - 1) - b * a.Hq, h = r / a.G, g = r - h * a.G;
-    const int b_lo = blockIdx.x * (kJoinWarps / W) / a.Hq;  // (the CTA adds up the lengths once)
-    int total = 0, u0 = 0;
+    constexpr int kPer = kJoinWarps / W;  // rows of a block
+    // (MANY: several blocks a CTA; a kernel of its own, since with the loop the others have fewer loads
+    // in flight: one sequence 8.3 us with one block a CTA, 9.6 with the loop)
+    const long long blocks = MANY ? (rows + kPer - 1) / kPer : gridDim.x;
+    const int blk0 = (int)(blocks * blockIdx.x / gridDim.x), blk1 = (int)(blocks * (blockIdx.x + 1) / gridDim.x);
+    // Where the rows' pieces lie follows from the lengths, which the kernels before this
+    // one only read: the first block's are found before the wait on them.
+    int b_at = blk0 * kPer / a.Hq;  // (the CTA adds up the lengths once)
+    int total = 0, u_at = 0;        // u_at: the first slot of sequence b_at
     for (int i = threadIdx.x; i < a.c.B; i += 32 * kJoinWarps) {
         const int v = span_of<GATHER>(a, i, false).slots() * a.c.Hkv;
         total += v;
-        if (i < b_lo) u0 += v;
+        if (i < b_at) u_at += v;
     }
     total = __reduce_add_sync(0xffffffffu, total);
-    u0 = __reduce_add_sync(0xffffffffu, u0);
-    if (lane == 0) red[warp] = make_int2(total, u0);
+    u_at = __reduce_add_sync(0xffffffffu, u_at);
+    if (lane == 0) red[warp] = make_int2(total, u_at);
     __syncthreads();
-    total = u0 = 0;
+    total = u_at = 0;
 #pragma unroll
-    for (int i = 0; i < kJoinWarps; ++i) total += red[i].x, u0 += red[i].y;
-    for (int i = b_lo; i < b; ++i) u0 += span_of<GATHER>(a, i, false).slots() * a.c.Hkv;
-    const Span s = span_of<GATHER>(a, b, false);
+    for (int i = 0; i < kJoinWarps; ++i) total += red[i].x, u_at += red[i].y;
     const Shares share = shares_of(a, total);
-    u0 += h * s.slots();  // the unit's first slot
-    const bool some = s.granules() > 0;
-    const int c0 = some ? share.cta_of(u0) : 0, c1 = some ? share.cta_of(u0 + s.granules() - 1) : 0;
-    const int first = 2 * c0 + (u0 > share.start(c0) ? 1 : 0);  // its first piece; the others are their CTAs' first
-    griddep_wait();
-    griddep_launch();
-    if (mine) {
-        const int n0 = s.lo > 0 ? a.pre.splits : 0;
-        const bool own = some && c0 == c1;
-        const int n = n0 + (some ? c1 - c0 + 1 : 0);
-        auto part = [&](int i) -> const float* {
-            if (i < n0) return a.pre.parts + ((long long)i * rows + row) * kPartFloats;
-            if (own) return a.own + (long long)row * kPartFloats;
-            return a.pieces + ((long long)(i == n0 ? first : (c0 + i - n0) * 2) * a.G + g) * kPartFloats;
-        };
-        mine = !(own && !a.own);
-        if (mine) o = join_sums(n, w, W, part, wts[warp], lane, [&] { join_weights(n, part, wts[warp], lane, &M, &L); });
-    }
-    if constexpr (W > 1) {
-        sums[warp][lane] = o;
-        __syncthreads();
-#pragma unroll
-        for (int i = 1; i < W; ++i) {
-            const float4 v = sums[warp + i < kJoinWarps ? warp + i : warp][lane];
-            o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+    int blk = blk0;
+    do {
+        const int row = blk * kPer + warp / W;
+        const int b = min(row, rows - 1) / a.Hq, r = min(row, rows - 1) - b * a.Hq, h = r / a.G, g = r - h * a.G;
+        for (; b_at < b; ++b_at) u_at += span_of<GATHER>(a, b_at, false).slots() * a.c.Hkv;
+        const Span s = span_of<GATHER>(a, b, false);
+        const int u0 = u_at + h * s.slots();  // the unit's first slot
+        const bool some = s.granules() > 0;
+        const int c0 = some ? share.cta_of(u0) : 0, c1 = some ? share.cta_of(u0 + s.granules() - 1) : 0;
+        const int first = 2 * c0 + (u0 > share.start(c0) ? 1 : 0);  // its first piece; the others are their CTAs' first
+        if (blk == blk0) {
+            griddep_wait();
+            griddep_launch();
         }
-    }
-    if (mine && w == 0) finish_row<E>(a, row, o, M, L, lane);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        float M = kNegInf, L = 0.f;
+        bool mine = row < rows;
+        if (mine) {
+            const int n0 = s.lo > 0 ? a.pre.splits : 0;
+            const bool own = some && c0 == c1;
+            const int n = n0 + (some ? c1 - c0 + 1 : 0);
+            auto part = [&](int i) -> const float* {
+                if (i < n0) return a.pre.parts + ((long long)i * rows + row) * kPartFloats;
+                if (own) return a.own + (long long)row * kPartFloats;
+                return a.pieces + ((long long)(i == n0 ? first : (c0 + i - n0) * 2) * a.G + g) * kPartFloats;
+            };
+            mine = !(own && !a.own);
+            __syncwarp();  // (of the block before: the weights have been read)
+            if (mine) o = join_sums(n, w, W, part, wts[warp], lane, [&] { join_weights(n, part, wts[warp], lane, &M, &L); });
+        }
+        static_assert(W == 1 || !MANY);
+        if constexpr (W > 1) {
+            sums[warp][lane] = o;
+            __syncthreads();
+#pragma unroll
+            for (int i = 1; i < W; ++i) {
+                const float4 v = sums[warp + i < kJoinWarps ? warp + i : warp][lane];
+                o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+            }
+        }
+        if (mine && w == 0) finish_row<E>(a, row, o, M, L, lane);
+    } while (MANY && ++blk < blk1);
 }
 
-template <class E, int W, bool GATHER>
+template <class E, int W, bool GATHER, bool MANY = false>
 static cudaError_t join_launch(const PgArgs& a, cudaStream_t st) {
-    const long long rows = (long long)a.c.B * a.Hq, per = kJoinWarps / W;
+    const long long rows = (long long)a.c.B * a.Hq, blocks = (rows * W + kJoinWarps - 1) / kJoinWarps;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((rows + per - 1) / per));
+    cfg.gridDim = dim3((unsigned)(MANY ? kJoinCtas : blocks));
     cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.stream = st;
     cudaLaunchAttribute attr[1] = {pdl_attr()};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_join_kernel<E, W, GATHER>, a, (int)rows);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_join_kernel<E, W, GATHER, MANY>, a, (int)rows);
     note_launch();
     return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -790,7 +809,8 @@ static cudaError_t join_pick(const PgArgs& a, cudaStream_t st) {
     const long long rows = (long long)a.c.B * a.Hq;
     if (rows <= 2 * kPagedSms) return join_launch<E, 8, GATHER>(a, st);
     if (rows <= 4 * kPagedSms) return join_launch<E, 4, GATHER>(a, st);
-    return join_launch<E, 1, GATHER>(a, st);
+    if (rows <= kJoinWarps * kJoinCtas) return join_launch<E, 1, GATHER>(a, st);
+    return join_launch<E, 1, GATHER, true>(a, st);
 }
 
 template <class E, int NT, bool GATHER>
