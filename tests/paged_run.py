@@ -91,3 +91,28 @@ def check_lse(lse, want, what=""):
     empty = np.isneginf(want)
     assert np.isneginf(got[empty]).all(), f"{what}: a sequence without a row has lse -inf"
     assert np.abs(got[~empty] - want[~empty]).max(initial=0.0) <= 2e-4, what
+
+
+def norm_tolerance(dtype, coarse_weights: bool) -> float:
+    """What the error of a row of O may be, relative to the row, both as norms over its 128 elements.
+
+    The output's rounding is off by half a step h of a value at most, h / sqrt(3) as a root mean square
+    (evenly spread over the step).  A weight's rounding, e_j <= h where a pass keeps the weights in
+    the element type, makes the error sum_j p_j e_j (v_j - O): with independent e_j and values of one
+    size its norm is the root mean square of e_j times |O|, h / sqrt(3) again; with 16 bits and more
+    it does not count.  The squares add up.  1.3: such a norm over 128 elements, or over the 100
+    rows and more that carry the weight, strays by 8 to 10% of its square, 4 times that at most
+    (over all rows of all tests); sums and logits in 32 bits (1e-5) lie in it too."""
+    return 1.3 * half_step(dtype) / np.sqrt(3.0) * np.sqrt(2.0 if coarse_weights else 1.0)
+
+
+def check_norm(O, want, lens, dtype, coarse_weights: bool, what=""):
+    """Each row of O [B, Hq, d] is within norm_tolerance of `want`, for sequences of 300 rows and more
+    (shorter ones: check_attn).  A bound by the largest value, as check_attn's, is as large as the
+    outputs themselves over thousands of rows."""
+    got, want = O.detach().cpu().double().numpy(), np.asarray(want)
+    long = np.asarray(lens) >= 300
+    assert long.any() and np.isfinite(got).all(), f"{what}: nothing to check, or non-finite output"
+    err = np.linalg.norm((got - want)[long], axis=-1) / np.linalg.norm(want[long], axis=-1)
+    tol = norm_tolerance(dtype, coarse_weights)
+    assert (err <= tol).all(), f"{what}: a row is off by {err.max():.2e} of its norm, allowed {tol:.2e}"
