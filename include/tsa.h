@@ -446,8 +446,14 @@ tsa_status tsa_paged_attn(const tsa_paged_attn_args* args, void* stream);
  * prefix (or a padding slot with len_b = 0) is attended through its own table alone,
  * and so is every sequence where the prefix is too short, or the batch too small, for
  * a pass of its own to pay: every sequence's table names its prefix's pages, too
- * (shared or copies of one another).  The result is tsa_paged_attn's, up to rounding.
- * prefix_len = 0: no shared rows; at most 2^30. */
+ * (shared or copies of one another).  prefix_len = 0: no shared rows; at most 2^30.
+ *
+ * Accuracy: the prefix has its own pass where (B - 1) * prefix_len * Hkv >= 81920 and
+ * the table reaches that far.  That pass rounds each softmax weight to the cache's type,
+ * once, before the product with V (sums and maxima stay in fp32), which makes the error
+ * of O about 1.4 times that of its own rounding to that type (of norms over a row).
+ * Elsewhere, and in tsa_paged_attn, weights keep 16 bits or more and the error is O's
+ * rounding.  A caller that wants those calls tsa_paged_attn over the same tables. */
 tsa_status tsa_prefix_attn(const tsa_paged_attn_args* args, void* stream);
 
 /* ------------------------------------------------------------------ status */

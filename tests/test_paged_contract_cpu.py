@@ -1,0 +1,51 @@
+"""What include/tsa.h says about the paged calls, held against the library."""
+import ctypes
+import os
+import re
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def tsa():
+    from top_sparse_attention_02_b200 import build
+
+    build.build()
+    from top_sparse_attention_02_b200 import binding
+
+    return binding
+
+
+@pytest.fixture(scope="module")
+def header():
+    return re.sub(r"\s*\n \*\s*", " ", open(os.path.join(ROOT, "include", "tsa.h")).read())
+
+
+def shape(tsa, B, Hkv, rows, page=16):
+    c = tsa.tsa_paged_cache()
+    for k, x in dict(page_stride=Hkv * page * 128, head_stride=page * 128, row_stride=128, num_pages=9, page_size=page,
+                     max_pages=-(-rows // page), B=B, Hkv=Hkv, d=128, dtype=0).items():
+        setattr(c, k, x)
+    return c
+
+
+@pytest.mark.parametrize("B,Hkv", [(2, 1), (2, 8), (9, 8), (33, 4), (641, 8), (1, 8)])
+def test_header_says_where_the_weights_are_coarser(tsa, header, B, Hkv):
+    """The pass with weights of the element type is the one that needs room for a prefix's partials:
+    from the product on that the header names, and not past the table's rows."""
+    at = re.search(r"\(B - 1\) \* prefix_len \* Hkv >= (\d+)", header)
+    assert at, "the header does not say from where on the prefix has its own pass"
+    first = -(-int(at.group(1)) // max(1, (B - 1) * Hkv))
+    c = shape(tsa, B, Hkv, 2 * first)
+    size = lambda n: tsa.lib().tsa_paged_workspace_size(ctypes.byref(c), 4 * Hkv, n)
+    assert size(first - 1) == size(0) > 0
+    assert (size(first) > size(0)) == (B > 1)
+    assert size(2 * first + 16) == size(0)  # no sequence can hold it
+
+
+def test_header_says_that_prefix_attention_may_round_its_weights(header):
+    text = header[header.index("for a batch whose sequences begin with the same prefix_len rows"):]
+    text = text[:text.index("tsa_status tsa_prefix_attn")]
+    assert "weight to the cache's type" in text and "tsa_paged_attn over the same tables" in text

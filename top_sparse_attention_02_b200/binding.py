@@ -496,5 +496,7 @@ def paged_attn(args: tsa_paged_attn_args, stream=None):
 
 
 def prefix_attn(args: tsa_paged_attn_args, stream=None):
-    """One token per sequence, the rows [0, prefix_len) that the batch shares read once for all."""
+    """One token per sequence, the rows [0, prefix_len) that the batch shares read once for all.  Over a
+    long enough prefix the softmax weights are rounded to the cache's type (include/tsa.h says from
+    where on); paged_attn over the same tables keeps 16 bits of them or more."""
     _launch(_lib.tsa_prefix_attn, args, stream)
