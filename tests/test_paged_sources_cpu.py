@@ -36,3 +36,13 @@ def test_inputs_that_the_kernel_before_may_write_are_not_restrict(name):
         for p in params.split(","):
             assert not ("const" in p and "__restrict__" in p), f"{kernel}: {p.strip()}"
     assert waits or name not in ("rope.cu", "paged.cu", "prefix.cu", "attn.cu", "topk.cu")
+
+
+def test_pages_of_a_prefix_are_looked_up_for_a_sequence_that_holds_it():
+    """tsa.h: table entries past a sequence's rows are not read.  The prefix pass reads entries of the
+    first sequence (a.table) under a test of its length, all others through `table`, the row of a
+    sequence that holds the prefix whole."""
+    (_, _, body), = kernels(os.path.join(CSRC, "prefix.cu"))
+    reads = [line for line in body.splitlines() if re.search(r"a\.table\[", line)]
+    assert reads and all("a.lens[0] >= a.prefix_len" in line for line in reads)
+    assert body.index("src < 0") < body.index("const int32_t* table = a.table") < body.index("= table[")

@@ -221,8 +221,10 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     }
     griddep_wait();
     griddep_launch();  // the pass over the sequences' own rows reads nothing of this one
-    // What needs no length is requested first: Q (all of a thread's loads at once;
-    // rows past R are zeros), and the first tiles' pages as the first sequence has them.
+    // Requested first: Q, which needs no length (all of a thread's loads at once; rows past
+    // R are zeros), and the first tiles' pages as the first sequence has them, if it holds
+    // the prefix (entries past a sequence's rows are not read; without that length in between
+    // few streams would take 18.2 us instead of 18.4).
     uint4 qv[kPxRows / 32];
     int pages = 0;
     const int ahead = 32 / chunks;  // tiles whose pages the producer's lanes hold
@@ -236,7 +238,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         }
     } else if (warp == 17) {
         const int r = (t0 + lane / chunks) * kPxTile + lane % chunks * box;
-        if (lane / chunks < nt && r < a.prefix_len) pages = a.table[r / a.page_size];
+        if (lane / chunks < nt && r < a.prefix_len && a.lens[0] >= a.prefix_len) pages = a.table[r / a.page_size];
     }
     // the sequence through whose table the prefix is read: the first that holds it whole
     int src = -1;
