@@ -155,10 +155,23 @@ struct Layout {
 };
 
 // Whether the prefix gets its own pass.  It saves reading the prefix's rows again for
-// every sequence but one, and costs 6 us (its set-up, and partials to join): measured,
-// 8 sequences x 512 rows x 8 kv-heads (28,672 rows saved) 12.0 us without it and 16.3 us
-// with it, 8 x 4096 x 8 (229,376) 25.0 and 18.2 us.  40 MB of K and V, 6 us at
-// HBM's rate, is 81,920 rows.
+// every sequence but one (out of L2, after the first), and costs its set-up and partials to
+// write and join.  Measured, us without and with it, page 64, 100 own rows a sequence:
+//
+//   rows saved, about    20,000     40,000     82,000    160,000    320,000
+//    4 x    32/8 heads   9.5 13.4  11.2 14.5  14.5 15.1  20.1 17.6  31.5 23.4
+//    8 x    32/8         9.6 12.7  11.0 13.8  13.9 15.5  19.1 16.5  28.6 18.4
+//   16 x    64/8        10.1 17.4  11.3 18.0  14.5 18.4  19.6 19.6  29.1 19.6
+//   32 x     8/8                   12.4 17.6  14.5 18.0  19.4 17.2  27.8 17.6
+//    8 x     8/2         9.2 12.0  10.4 13.0  13.7 13.3  18.4 14.9  28.3 16.8
+//   16 x     8/1         9.6 14.1  10.9 13.6  13.7 14.7  18.6 16.9  28.5 17.8
+//   64 x    32/8                   14.5 24.7  18.8 24.7  22.3 25.0  31.5 23.8
+//    2 x    32/8        10.2 13.7  12.7 14.8  17.2 20.1  26.0 28.3  42.8 45.4
+//
+// (graph replays; with cold caches the same within 2 us, but for two sequences, where it
+// is 24.6 28.7, 41.0 36.9, 69.6 54.3 in the last three columns).  So it pays from 80,000 to
+// 160,000 rows on, for 64 sequences and more from 250,000.  The bound is the lower end,
+// where tsa.h has it; between the two a call may lose up to 4 us (64 sequences: 6).
 bool shares(const tsa::Pages& c, int prefix_len) {
     return prefix_len > 0 && prefix_len <= c.rows_cap() && (c.B - 1LL) * prefix_len * c.Hkv >= 81920;
 }
