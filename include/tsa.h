@@ -372,7 +372,8 @@ typedef struct {
 
 /* Queries and keys of T tokens in one pass: the RMS norm of each head (over its d
  * elements, times a weight [d] fp32; a NULL weight leaves those heads unnormed), then
- * the rotation.  One rounding, at the end.  Heads of 128 elements at
+ * the rotation.  One rounding, at the end; a head's squares are summed in fp32 (elements
+ * of up to 1.6e18).  Heads of 128 elements at
  * token * stride_t + head * stride_h (elements, multiples of 8; 16-byte aligned
  * bases), so the queries and keys of one fused projection are read in place; an
  * output may be its own input (the same pointer and strides), and must not
@@ -429,7 +430,7 @@ typedef struct {
     float* lse;                 /* NULL or [B, Hq]: base-2 log-sum-exp of the scaled logits (-inf without a row) */
     int32_t Hq, k_max;
     int32_t prefix_len;         /* tsa_prefix_attn: the rows that the batch shares */
-    float scale;                /* finite, > 0 */
+    float scale;                /* > 0, at most 2.35e38 (scale * log2(e) is finite) */
     void* ws;
     size_t ws_bytes;
 } tsa_paged_attn_args;

@@ -49,3 +49,17 @@ def test_header_says_that_prefix_attention_may_round_its_weights(header):
     text = header[header.index("for a batch whose sequences begin with the same prefix_len rows"):]
     text = text[:text.index("tsa_status tsa_prefix_attn")]
     assert "weight to the cache's type" in text and "tsa_paged_attn over the same tables" in text
+
+
+def test_a_scale_without_a_finite_base_2_logarithm_is_refused(tsa):
+    """Scores are scale * log2(e) * <q, k>: with an infinite factor a product of 0 would be NaN."""
+    c = shape(tsa, 3, 2, 64)
+    c.K, c.V, c.page_table = 0x10000, 0x20000, 0x30000
+    a = tsa.tsa_paged_attn_args()
+    a.cache = c
+    for k, x in dict(Q=0x40000, seq_lens=0x50000, O=0x60000, Hq=8, ws=0x100000, ws_bytes=0).items():
+        setattr(a, k, x)
+    for name in ("tsa_paged_attn", "tsa_prefix_attn"):
+        for scale, status, msg in ((3e38, 1, "scale"), (2.4e38, 1, "scale"), (2.35e38, 3, "needs"), (1e-45, 3, "needs")):
+            a.scale = scale
+            assert getattr(tsa.lib(), name)(ctypes.byref(a), None) == status and msg in tsa.last_error(), (name, scale)

@@ -117,3 +117,16 @@ def test_replayed_steps_attend_to_the_row_they_append(cuda_dev, dt, shared):
         check_norm(O, want, at, DT[dt], shared, f"step {n}")
         check_lse(lse, wl, f"step {n}")
     del graph
+
+
+@pytest.mark.parametrize("dt,size", [("bf16", 1.5e18), ("bf16", 1e-16), ("fp16", 6e4), ("fp16", 6e-8)])
+def test_norm_over_the_range_of_elements(cuda_dev, dt, size):
+    """The largest elements whose squares' sum fp32 holds, and the smallest ones, without an eps."""
+    g = torch.Generator().manual_seed(3)
+    x = ((torch.rand(33, 6, 128, generator=g, dtype=torch.float64) * 2 - 1) * size).to(DT[dt]).to(cuda_dev)
+    x[:, :, 0] = size
+    w, f = 1 + 0.2 * torch.randn(128, generator=g), freqs(64, cuda_dev)
+    pos = torch.arange(33, dtype=torch.int32, device=cuda_dev) * 77
+    o = torch.empty_like(x)
+    tsa.qk_norm_rope(tsa.qk_norm_rope_args(x, None, o, None, q_weight=w.to(cuda_dev), eps=0.0, positions=pos, inv_freq=f))
+    check_rounded(o, oracle.norm_rope(x, w, 0.0, pos.cpu(), f, False), DT[dt], f"{size}")

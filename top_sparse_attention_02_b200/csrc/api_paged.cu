@@ -7,6 +7,7 @@
 #include <cstdarg>
 #include <cstdio>
 
+#include "common.cuh"
 #include "paged.h"
 #include "tsa.h"
 
@@ -194,8 +195,8 @@ tsa_status attn(const tsa_paged_attn_args* a, bool prefix, const char* what, voi
     tsa::Pages c;
     TSA_TRY(check_cache(a->cache, &c));
     TSA_TRY(check_group(a->Hq, c.Hkv));
-    if (!std::isfinite(a->scale) || !(a->scale > 0.f))
-        return fail(TSA_ERR_INVALID_ARG, "%s: scale must be finite and > 0 (got %g)", what, (double)a->scale);
+    if (!std::isfinite(a->scale * tsa::kLog2e) || !(a->scale > 0.f))  // (the kernels' scores are in base 2)
+        return fail(TSA_ERR_INVALID_ARG, "%s: scale must be > 0 and scale * log2(e) finite (got %g)", what, (double)a->scale);
     if (a->prefix_len < 0 || (!prefix && a->prefix_len != 0))
         return fail(TSA_ERR_INVALID_ARG, "%s: prefix_len must be %s (got %d)", what, prefix ? ">= 0" : "0", a->prefix_len);
     if (prefix && (a->idx || a->k_per_seq))
