@@ -437,6 +437,8 @@ typedef struct {
 
 /* One token per sequence over its pages: every row, or (a layer that reuses
  * an earlier layer's indices) the rows of an index list as tsa_decode_step writes it.
+ * (That step selects over a contiguous bf16 cache, which is one page a sequence here;
+ * over other pages the lists are the caller's.)
  * prefix_len must be 0. */
 tsa_status tsa_paged_attn(const tsa_paged_attn_args* args, void* stream);
 

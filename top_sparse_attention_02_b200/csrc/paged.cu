@@ -35,7 +35,7 @@
 //
 // Measured (graph replays): 64 sequences of 8192 to 32768 rows, 64/8 heads (5.18 GB) 805 us =
 // 6.44 TB/s, HBM's rate; 17 ragged sequences, 40/8 heads, 139 MB 28.5 us = 4.9 TB/s; one
-// sequence of 4096 rows, 2 kv-heads 8.2 us; 2621 selected rows of 8 kv-heads at 131072 (10.7 MB)
+// sequence of 4096 rows, 2 kv-heads 8.3 us; 2621 selected rows of 8 kv-heads at 131072 (10.7 MB)
 // 9.9 us.  The last two are a chain of waits: lengths 0.9 us, pages (or list, then pages) 1 to 2,
 // rows 0.4, products and the warps' merge 1.5 (marks of SM time); the second kernel is the rest.
 //
@@ -803,7 +803,8 @@ static cudaError_t join_launch(const PgArgs& a, cudaStream_t st) {
 // The whole call with 1, 4 and 8 warps a row, us: 8 rows of 60 pieces 16.3, 10.0, 8.2;
 // 256 rows of a shared prefix 20.6, 18.8, 18.9; 320 rows of it 21.2, 19.2, 21.6; 512 rows
 // (a prefix of 16384) 35.8, 28.9, 33.4; 768 rows 26.2, 26.6, 30.3, and without a prefix
-// 37.7, 41.5, 44.3; 1024 rows 30.1, 33.4, 38.4; 4096 rows 121.7, 136, 157.
+// 37.7, 41.5, 44.3; 1024 rows 30.1, 33.4, 38.4; 4096 rows 121.7, 136, 157.  (The form with 4
+// has 128 registers and spills 8 bytes.)
 template <class E, bool GATHER>
 static cudaError_t join_pick(const PgArgs& a, cudaStream_t st) {
     const long long rows = (long long)a.c.B * a.Hq;

@@ -33,8 +33,9 @@
 // long.  The outputs' error is then 1.4 times their own rounding's (2.3e-3 against 1.7e-3 of
 // the norm in bf16), the weights' errors being independent.
 //
-// Measured: 64 sequences x 64/8 heads over 32768 rows (68.7 Gflop, 134 MB) 79 us with the join = 0.87 PFLOP/s,
-// 0.53 of the measured matrix rate.  A pair of tiles takes 3870 cycles where their products take
+// Measured: 64 sequences x 64/8 heads over 32768 rows (68.7 Gflop, 134 MB) 82 us with the join = 0.84 PFLOP/s,
+// 0.51 of the measured matrix rate.  At 96 registers the softmax spills 44 bytes (100 of loads).  With
+// fused products of scores (2% faster) a pair of tiles took 3870 cycles where their products take
 // 2068: each stream is a chain of softmax (2150, of which the special-function units need
 // 1024), turn, products and their waits (1700), and TMEM has no room for S of a third tile.  Half tiles (64 columns) with S two
 // halves ahead came to 4140 (one thread a row) and 3870 (two groups in turn); a part of the

@@ -20,10 +20,11 @@
 // (A CTA of 256 threads that shared the angles of 4 tokens through a barrier, in
 // 110 registers, took 72 us for the first of the cases below.)
 //
-// Measured: 8192 tokens x 40 heads, split pairs (168 MB) 34 us = 4.9 TB/s, where a plain
-// copy of those bytes takes 27; 4099 x 72 heads, interleaved (151 MB) 26.5 us = 5.7 TB/s;
-// appending 16348 tokens of 8 + 8 heads (134 MB) 22.6 us = 5.9 TB/s; one token 2.8 us, a
-// launch.  A plain copy of 67 to 84 MB runs at 6.0 to 6.1 TB/s.  Split pairs use 67% of the
+// Measured (graph replays, a part of the data warm in L2; in brackets calls on inputs that
+// are not): 8192 tokens x 40 heads, split pairs (168 MB) 33.8 us = 5.0 TB/s [35.7], where a
+// plain copy of those bytes takes 27; 4099 x 72 heads, interleaved (151 MB) 26.9 us [28.6];
+// appending 16348 tokens of 8 + 8 heads (134 MB) 22.9 us [24.6]; one token 2.8 us [3.8], a
+// launch.  A plain copy of 67 to 84 MB runs at 6.0 to 6.1 TB/s.  Split pairs use 65% of the
 // issue slots (140 instructions a pair of heads, the partners' shuffles among them) and
 // 43% of HBM.  Walking the heads by pointers instead of indexes took 37.8 and 33.9 us.
 #include <cuda_fp16.h>
