@@ -63,3 +63,21 @@ def test_a_scale_without_a_finite_base_2_logarithm_is_refused(tsa):
         for scale, status, msg in ((3e38, 1, "scale"), (2.4e38, 1, "scale"), (2.35e38, 3, "needs"), (1e-45, 3, "needs")):
             a.scale = scale
             assert getattr(tsa.lib(), name)(ctypes.byref(a), None) == status and msg in tsa.last_error(), (name, scale)
+
+
+def test_the_stride_of_a_dimension_of_one_does_not_matter(tsa):
+    """One page, or one head: what torch reports as its stride depends on where the tensor came from."""
+    import torch
+
+    table = torch.zeros(2, 1, dtype=torch.int32)
+    pool = torch.zeros(4, 2, 2, 16, 128, dtype=torch.bfloat16)
+    K, V = pool[1:2, 0], torch.zeros(1, 2, 16, 128, dtype=torch.bfloat16)  # one page: strides 8192 and 4096
+    assert K.stride(0) != V.stride(0)
+    c = tsa.paged_cache(K, V, table)
+    assert (c.head_stride, c.row_stride) == (2048, 128)
+    K, V = pool[:, 0, :1], torch.zeros(4, 2, 1, 16, 128, dtype=torch.bfloat16)[:, 0]  # one head
+    with pytest.raises(tsa.TsaError, match="same strides"):
+        tsa.paged_cache(K, V, table)  # (the pages' strides differ: 8192 and 4096)
+    size = lambda c: tsa.lib().tsa_paged_workspace_size(ctypes.byref(c), 0, 0)
+    c = tsa.paged_cache(pool[:, 0, :1], pool[:, 1, 1:], table)
+    assert size(c) == 256

@@ -361,7 +361,8 @@ def paged_cache(K_pages, V_pages, page_table) -> tsa_paged_cache:
     dev = K_pages.device
     _tensor(K_pages, "K_pages", K_pages.dtype, (None,) * 4, dev, contiguous=False)
     _tensor(V_pages, "V_pages", K_pages.dtype, K_pages.shape, dev, contiguous=False)
-    _need(K_pages.stride() == V_pages.stride(), "K_pages and V_pages must have the same strides")
+    _need(all(n == 1 or a == b for n, a, b in zip(K_pages.shape, K_pages.stride(), V_pages.stride())),
+          "K_pages and V_pages must have the same strides")  # (a dimension of one has none)
     _tensor(page_table, "page_table", torch.int32, (None, None), dev)
     c = tsa_paged_cache()
     c.K, c.V, c.page_table = K_pages.data_ptr(), V_pages.data_ptr(), page_table.data_ptr()
