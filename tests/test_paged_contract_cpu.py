@@ -81,3 +81,17 @@ def test_the_stride_of_a_dimension_of_one_does_not_matter(tsa):
     size = lambda c: tsa.lib().tsa_paged_workspace_size(ctypes.byref(c), 0, 0)
     c = tsa.paged_cache(pool[:, 0, :1], pool[:, 1, 1:], table)
     assert size(c) == 256
+
+
+def test_a_prefix_length_past_32_bits_is_refused(tsa):
+    """It is not cut to its low 32 bits."""
+    import torch
+
+    K, table = torch.zeros(4, 2, 16, 128, dtype=torch.bfloat16), torch.zeros(2, 2, dtype=torch.int32)
+    Q, lens, ws = torch.zeros(2, 4, 128, dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int32), torch.zeros(1 << 16, dtype=torch.uint8)
+    c = tsa.paged_cache(K, K, table)
+    for n in (2 ** 32 + 16, 2 ** 31, -2 ** 31 - 1):
+        with pytest.raises(tsa.TsaError, match="prefix_len"):
+            tsa.paged_attn_args(c, Q, lens, Q.clone(), ws, scale=0.1, prefix_len=n)
+        with pytest.raises(tsa.TsaError, match="prefix_len"):
+            tsa.paged_workspace_size(c, 4, n)

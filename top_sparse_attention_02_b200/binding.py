@@ -375,6 +375,7 @@ def paged_cache(K_pages, V_pages, page_table) -> tsa_paged_cache:
 
 
 def paged_workspace_size(cache: tsa_paged_cache, Hq: int = 0, prefix_len: int = 0) -> int:
+    _need(-2 ** 31 <= prefix_len < 2 ** 31, f"prefix_len={prefix_len} does not fit 32 bits")
     n = _lib.tsa_paged_workspace_size(ctypes.byref(cache), Hq, prefix_len)
     if n == 0:
         raise TsaError(TSA_ERR_INVALID_ARG, last_error())
@@ -484,6 +485,7 @@ def paged_attn_args(cache: tsa_paged_cache, Q, seq_lens, O, ws, *, scale: float,
     if lse is not None:
         _tensor(lse, "lse", torch.float32, Q.shape[:2], dev)
         a.lse = lse.data_ptr()
+    _need(-2 ** 31 <= prefix_len < 2 ** 31, f"prefix_len={prefix_len} does not fit 32 bits")  # (ctypes would cut it)
     _tensor(ws, "ws", torch.uint8, (None,), dev)
     a.Q, a.O, a.seq_lens = Q.data_ptr(), O.data_ptr(), seq_lens.data_ptr()
     a.Hq, a.prefix_len, a.scale = Q.shape[1], prefix_len, scale
